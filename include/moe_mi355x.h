@@ -60,6 +60,7 @@ extern "C" {
 #define MOE_MAX_EXPERTS 1024   /* routed + shared experts */
 #define MOE_MAX_K 16           /* routed experts per token */
 #define MOE_TILE_ROWS 256      /* rows per entry of the GEMM tile map */
+#define MOE_NORM_MAX_D 32768   /* columns of moe_rmsnorm */
 
 typedef enum {
   MOE_OK = 0,
@@ -544,6 +545,64 @@ moe_status moe_route_backward(const void* grad_out, moe_dtype g_t, const void* d
                               const int32_t* seg_offset, const int32_t* row_token,
                               int T, int d, int K, int Nr, int Ns,
                               void* du, moe_dtype du_t, float* de, void* stream);
+
+/* ========================================================================
+ * Entering the layer: the root-mean-square norm of a pre-norm block.
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * moe_rmsnorm: residual addition, root-mean-square norm and E4M3 tiles in
+ * one pass over the rows:
+ *   r = x + resid,  c = (mean_j r_j^2 + eps)^(-1/2),  u_j = r_j c w_j
+ * in fp32 (sum of squares included); each output is rounded once, from the
+ * fp32 value (u and the codes from the unrounded r).
+ *   x, x_t       device [T, d], MOE_F32 or MOE_BF16
+ *   resid, r_t   device [T, d] or NULL (r = x), MOE_F32 or MOE_BF16
+ *   weight, w_t  device [d], MOE_F32 or MOE_BF16
+ *   eps          finite, >= 0
+ *   r_out        device [T, d] out of type r_t, or NULL; may be resid, or x
+ *                where x_t == r_t (r_t is not read when resid and r_out are
+ *                NULL)
+ *   u, u_t       device [T, d] out, MOE_F32 or MOE_BF16, or NULL when q is
+ *                given; may be x where x_t == u_t
+ *   q, q_scale   device [T, d] uint8 and [T, d/128] fp32 out: u in 1x128
+ *                E4M3 tiles by the rule of fp8_quantize_tiles, or both NULL
+ *   rstd         device [T] fp32 out: c, for moe_rmsnorm_backward; or NULL
+ * A row of zeros with eps == 0 gives NaN, as the formula does.
+ *   Errors: MOE_EINVAL for NULL pointers, bad sizes or types, d % 8 != 0 (d %
+ *   128 != 0 with q), a misaligned tensor; MOE_EUNSUPPORTED for d >
+ *   MOE_NORM_MAX_D.  T == 0 is valid: nothing is written.
+ * ---------------------------------------------------------------------- */
+moe_status moe_rmsnorm(const void* x, moe_dtype x_t, const void* resid, moe_dtype r_t,
+                       const void* weight, moe_dtype w_t, float eps, long long T, int d,
+                       void* r_out, void* u, moe_dtype u_t, uint8_t* q, float* q_scale,
+                       float* rstd, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_rmsnorm_backward: gradients of moe_rmsnorm, with xhat = r c and
+ * g = du w:
+ *   dx_j = dr_j + c (g_j - xhat_j mean_i(g_i xhat_i))   (of x and of resid)
+ *   dw_j = sum_t du_tj xhat_tj
+ * in fp32.  Codes q carry no gradient of their own: du is the gradient of u
+ * (straight through the quantiser).
+ *   du, du_t     device [T, d], MOE_F32 or MOE_BF16
+ *   r, r_t       device [T, d], MOE_F32 or MOE_BF16: r_out of the forward (x
+ *                when it had no residual)
+ *   weight, w_t  device [d]; rstd device [T] fp32 from the forward
+ *   dr           device [T, d] of type r_t: gradient that reaches r along the
+ *                residual stream, or NULL (zero)
+ *   dx           device [T, d] of type r_t out; may be dr, or du where
+ *                du_t == r_t
+ *   dw           device [d] fp32 out (overwritten), summed in a fixed order
+ *   ws           device, moe_rmsnorm_backward_workspace_bytes(T, d) bytes
+ *   Errors: as moe_rmsnorm; MOE_EWORKSPACE for a small ws.  T == 0 is valid:
+ *   dw is zeroed.
+ * ---------------------------------------------------------------------- */
+size_t moe_rmsnorm_backward_workspace_bytes(long long T, int d);
+moe_status moe_rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t,
+                                const void* weight, moe_dtype w_t, const float* rstd,
+                                const void* dr, long long T, int d, void* dx, float* dw,
+                                void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,7 @@ MOE_COMBINE_NO_RESIDUAL, MOE_COMBINE_NO_SHARED, MOE_COMBINE_NO_ROUTED = 1, 2, 4
 MOE_TILE_ROWS = 256
 MOE_MAX_K = 16
 MOE_MAX_EXPERTS = 1024
+MOE_NORM_MAX_D = 32768
 
 # Every symbol the header declares, with its ctypes signature.
 _vp, _i, _ll, _sz, _f, _u = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint
@@ -64,6 +65,9 @@ SIGNATURES = {
     "fp8_quantize_runs_max": (_ll, [_ll, _i]),
     "fp8_quantize_runs": (_i, [_vp, _i, _ll, _i, _vp, _i, _vp, _i, _ll, _vp, _vp, _vp, _vp]),
     "moe_route_backward": (_i, [_vp, _i, _vp, _vp, _i] + [_vp] * 7 + [_i] * 5 + [_vp, _i, _vp, _vp]),
+    "moe_rmsnorm": (_i, [_vp, _i, _vp, _i, _vp, _i, _f, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
+    "moe_rmsnorm_backward_workspace_bytes": (_sz, [_ll, _i]),
+    "moe_rmsnorm_backward": (_i, [_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _ll, _i, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -334,6 +338,60 @@ def fp8_dequantize_tiles(q, scale, tile_rows, out, tile_cols=128, stream=None):
     rows = q.numel() // cols if cols else 0
     _check(lib().fp8_dequantize_tiles(_ptr(q), _ptr(scale), rows, cols, tile_rows, tile_cols, _ptr(out),
                                       dtype_code(out), _stream(stream)))
+
+
+def _same(t, like, name, dtype=None):
+    """t has `like`'s shape (and `dtype`): a kernel reads and writes that many elements of it."""
+    if t is not None and (t.shape != like.shape or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{name}: expected {tuple(like.shape)}{'' if dtype is None else f' {dtype}'}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _shape(t, shape, dtype, name):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def moe_rmsnorm(x, weight, eps, residual=None, r_out=None, u=None, q=None, q_scale=None, rstd=None, stream=None):
+    """r = x + residual, u = r (mean r^2 + eps)^(-1/2) weight, in one pass
+    over the rows of x [T, d]: writes r_out (of residual's dtype, or x's), u,
+    u's 1x128 E4M3 tiles q / q_scale and rstd [T], each where given."""
+    T, d = x.shape
+    r_t = MOE_F32
+    for t, name in ((residual, "residual"), (r_out, "r_out")):
+        _same(t, x, name)
+        if t is not None:
+            r_t = dtype_code(t)
+    if residual is not None and r_out is not None and residual.dtype != r_out.dtype:
+        raise ValueError("r_out must have residual's dtype")
+    _shape(weight, (d,), weight.dtype, "weight")
+    _same(u, x, "u")
+    _same(q, x, "q", torch.uint8)
+    _shape(q_scale, (T, d // 128), torch.float32, "q_scale")
+    _shape(rstd, (T,), torch.float32, "rstd")
+    _check(lib().moe_rmsnorm(_ptr(x), dtype_code(x), _ptr(residual), r_t, _ptr(weight), dtype_code(weight), eps, T, d,
+                             _ptr(r_out), _ptr(u), MOE_F32 if u is None else dtype_code(u), _ptr(q), _ptr(q_scale),
+                             _ptr(rstd), _stream(stream)))
+
+
+def moe_rmsnorm_backward_workspace_bytes(T, d):
+    return lib().moe_rmsnorm_backward_workspace_bytes(T, d)
+
+
+def moe_rmsnorm_backward(du, r, weight, rstd, dr, dx, dw, ws, stream=None):
+    """Gradients of moe_rmsnorm: dx [T, d] (of x and of the residual; dr, the
+    gradient along the residual stream, is added when given) and dw [d] fp32.
+    r, dr and dx share a dtype."""
+    T, d = r.shape
+    _same(du, r, "du")
+    _same(dr, r, "dr", r.dtype)
+    _same(dx, r, "dx", r.dtype)
+    _shape(weight, (d,), weight.dtype, "weight")
+    _shape(rstd, (T,), torch.float32, "rstd")
+    _shape(dw, (d,), torch.float32, "dw")
+    _check(lib().moe_rmsnorm_backward(_ptr(du), dtype_code(du), _ptr(r), dtype_code(r), _ptr(weight),
+                                      dtype_code(weight), _ptr(rstd), _ptr(dr), T, d, _ptr(dx), _ptr(dw), _ptr(ws),
+                                      _nbytes(ws), _stream(stream)))
 
 
 # ------------------------------------------------------- layer plumbing --

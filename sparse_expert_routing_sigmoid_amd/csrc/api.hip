@@ -86,6 +86,13 @@ moe_status route_backward(const void* grad_out, moe_dtype g_t, const void* dx, c
                           const float* centroids, const int32_t* topk_idx, const int32_t* inv_row, const float* dz,
                           const float* dz_row, const int32_t* seg_offset, const int32_t* row_token, int T, int d,
                           int K, int Nr, int Ns, void* du, moe_dtype du_t, float* de, void* stream);
+moe_status rmsnorm(const void* x, moe_dtype x_t, const void* resid, moe_dtype r_t, const void* w, moe_dtype w_t,
+                   float eps, long long T, int d, void* r_out, void* u, moe_dtype u_t, uint8_t* q, float* q_scale,
+                   float* rstd, void* stream);
+size_t rmsnorm_backward_workspace_bytes(long long T, int d);
+moe_status rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t, const void* w, moe_dtype w_t,
+                            const float* rstd, const void* dr, long long T, int d, void* dx, float* dw, void* ws,
+                            size_t ws_bytes, void* stream);
 
 namespace {
 thread_local std::string g_last_error;
@@ -318,6 +325,22 @@ moe_status moe_route_backward(const void* grad_out, moe_dtype g_t, const void* d
   moe::clear_error();
   return moe::route_backward(grad_out, g_t, dx, u, u_t, centroids, topk_idx, inv_row, dz, dz_row, seg_offset,
                              row_token, T, d, K, Nr, Ns, du, du_t, de, stream);
+}
+
+moe_status moe_rmsnorm(const void* x, moe_dtype x_t, const void* resid, moe_dtype r_t, const void* weight,
+                       moe_dtype w_t, float eps, long long T, int d, void* r_out, void* u, moe_dtype u_t, uint8_t* q,
+                       float* q_scale, float* rstd, void* stream) {
+  moe::clear_error();
+  return moe::rmsnorm(x, x_t, resid, r_t, weight, w_t, eps, T, d, r_out, u, u_t, q, q_scale, rstd, stream);
+}
+
+size_t moe_rmsnorm_backward_workspace_bytes(long long T, int d) { return moe::rmsnorm_backward_workspace_bytes(T, d); }
+
+moe_status moe_rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t, const void* weight,
+                                moe_dtype w_t, const float* rstd, const void* dr, long long T, int d, void* dx,
+                                float* dw, void* ws, size_t ws_bytes, void* stream) {
+  moe::clear_error();
+  return moe::rmsnorm_backward(du, du_t, r, r_t, weight, w_t, rstd, dr, T, d, dx, dw, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

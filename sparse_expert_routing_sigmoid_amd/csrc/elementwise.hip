@@ -5,6 +5,7 @@
 // section 2 (combine equation, bias rule with gamma = 0.001) and "Key ideas",
 // FP8 bullet (E4M3, 1x128 activation tiles, 128x128 weight blocks).
 #include "common.h"
+#include "vec8.h"
 
 namespace moe {
 
@@ -14,80 +15,6 @@ namespace {
 // One block per token and 2048-column chunk; every thread owns 8 consecutive
 // columns (16 B of bf16), so all loads are 16 B and coalesced.  The sum runs
 // in fp32 in a fixed order: residual, shared experts, routed slots 0..K-1.
-template <typename T_>
-struct Vec8;
-template <>
-struct Vec8<uint16_t> {
-  __device__ static void load(const uint16_t* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-  __device__ static void store(uint16_t* p, const float (&v)[8]) {
-    uint4 q;
-    q.x = pack_bf16x2(v[0], v[1]);
-    q.y = pack_bf16x2(v[2], v[3]);
-    q.z = pack_bf16x2(v[4], v[5]);
-    q.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4*>(p) = q;
-  }
-};
-template <>
-struct Vec8<float> {
-  __device__ static void load(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  __device__ static void store(float* p, const float (&v)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  }
-};
-
-// Raw 8-element vectors, kept as loaded until they are added (bf16 rows take
-// 4 registers instead of 8).  Every byte is read once, so the loads are
-// non-temporal (264 -> 231 us for the combine at T = 8192, d = 7168).
-typedef unsigned u32x4_nt __attribute__((ext_vector_type(4)));
-typedef float f32x4_nt __attribute__((ext_vector_type(4)));
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-  uint4 q;
-  __device__ void load(const uint16_t* p) {
-    const u32x4_nt v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_nt*>(p));
-    q = make_uint4(v.x, v.y, v.z, v.w);
-  }
-  __device__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-};
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ void load(const float* p) {
-    const f32x4_nt x = __builtin_nontemporal_load(reinterpret_cast<const f32x4_nt*>(p));
-    const f32x4_nt y = __builtin_nontemporal_load(reinterpret_cast<const f32x4_nt*>(p + 4));
-    a = make_float4(x.x, x.y, x.z, x.w);
-    b = make_float4(y.x, y.y, y.z, y.w);
-  }
-  __device__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-};
-
 constexpr int CB_THREADS = 128;
 constexpr int CB_COLS = CB_THREADS * 8;  // 1024 columns per block: d = 7168 is 7 blocks
 constexpr int CB_SHARED = 2;              // shared rows gathered up front (more are added one by one)

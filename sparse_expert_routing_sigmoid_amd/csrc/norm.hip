@@ -1,0 +1,368 @@
+// Root-mean-square norm in front of an expert layer, with the residual's
+// addition and the 1x128 E4M3 tiles of its output, and its gradient.
+//
+//   r = x + resid,  c = (mean_j r_j^2 + eps)^(-1/2),  u = r c w
+//   xhat = r c, g = du w:  dx = dr + c (g - xhat mean_j(g_j xhat_j)),
+//                          dw_j = sum_t du_tj xhat_tj
+// Both are bound by HBM: every operand is read once and every result written
+// once, the row living in registers between the reduction and its use (a
+// thread holds C chunks of 8 columns; TPR threads share a row).  A thread
+// has read all it needs of a row before it writes any of it, so a result may
+// lie on an operand of its own type.
+#include "common.h"
+#include "vec8.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int NORM_MAX_D = 1024 * 4 * 8;
+
+template <int TPR>
+constexpr int norm_threads() {
+  return TPR < 256 ? 256 : TPR;
+}
+
+// Sum of v over the TPR threads of a row.  `red` holds one value per wave for
+// two rows in turn, so one barrier a row is enough: a wave that writes the
+// next row's slot has passed the barrier after which the others read this
+// row's, and the slot after that is two barriers away.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (&red)[2][16], int parity) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  if (TPR == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[parity][threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = red[parity][0];
+#pragma unroll
+  for (int i = 1; i < TPR / 64; ++i) s += red[parity][i];
+  return s;
+}
+
+__device__ __forceinline__ void load_w8(const void* w, bool bf16, int c, float (&v)[8]) {
+  if (bf16)
+    Vec8<uint16_t>::load(static_cast<const uint16_t*>(w) + c, v);
+  else
+    Vec8<float>::load(static_cast<const float*>(w) + c, v);
+}
+
+template <typename XT, typename RT, int TPR, int C>
+__global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm(
+    const XT* x, const RT* resid, const void* __restrict__ w, bool w_bf16, float eps, long long T, int d, RT* r_out,
+    void* u, bool u_bf16, uint8_t* __restrict__ q,
+    float* __restrict__ q_scale, float* __restrict__ rstd) {
+  __shared__ float red[2][16];
+  constexpr int RPB = norm_threads<TPR>() / TPR;  // rows a block works on at a time
+  const int tid = threadIdx.x % TPR;
+  int col[C];
+  bool live[C];
+  float wv[C][8];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    col[j] = (j * TPR + tid) * 8;
+    live[j] = col[j] < d;
+    if (live[j]) load_w8(w, w_bf16, col[j], wv[j]);
+  }
+  int parity = 0;
+  for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < T; row += (long long)gridDim.x * RPB) {
+    const long long o = row * d;
+    float v[C][8];
+    Raw8<XT> rx[C];
+    Raw8<RT> rr[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (live[j]) {
+        rx[j].load(x + o + col[j]);
+        if (resid) rr[j].load(resid + o + col[j]);
+      }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (live[j]) {
+        rx[j].get(v[j]);
+        if (resid) {
+          float t[8];
+          rr[j].get(t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j][i] += t[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(v[j][i], v[j][i], s);
+      }
+    s = row_sum<TPR>(s, red, parity);
+    parity ^= 1;
+    const float c = 1.0f / sqrtf(s / (float)d + eps);
+    if (rstd && tid == 0) rstd[row] = c;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      // 16 consecutive threads hold a 1x128 tile: all live or none (d % 128
+      // == 0 where tiles are asked for)
+      if (live[j]) {
+        if (r_out) Vec8<RT>::store(r_out + o + col[j], v[j]);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = v[j][i] * c * wv[j][i];
+        if (u) {
+          if (u_bf16)
+            Vec8<uint16_t>::store(static_cast<uint16_t*>(u) + o + col[j], y);
+          else
+            Vec8<float>::store(static_cast<float*>(u) + o + col[j], y);
+        }
+        if (q) {
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));
+#pragma unroll
+          for (int off = 1; off < 16; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+          const int k = pow2_scale_exp(amax);
+          const float inv = exp2_int(-k);
+          uint2 code;
+          code.x = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+          code.y = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+          *reinterpret_cast<uint2*>(q + o + col[j]) = code;
+          if ((tid & 15) == 0) q_scale[(o + col[j]) >> 7] = exp2_int(k);
+        }
+      }
+    }
+  }
+}
+
+// dx of every row, and this row group's part of dw: rows first, first +
+// groups, ... are added in that order in registers, the row groups later in
+// the order of their number (k_norm_dw), so dw is bitwise reproducible.
+template <typename GT, typename RT, int TPR, int C>
+__global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
+    const GT* du, const RT* r, const void* __restrict__ w, bool w_bf16, const float* __restrict__ rstd, const RT* dr,
+    long long T, int d, RT* dx, float* __restrict__ part) {
+  __shared__ float red[2][16];
+  constexpr int RPB = norm_threads<TPR>() / TPR;
+  const int tid = threadIdx.x % TPR;
+  const long long group = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+  int col[C];
+  bool live[C];
+  float wv[C][8], dw[C][8];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    col[j] = (j * TPR + tid) * 8;
+    live[j] = col[j] < d;
+    if (live[j]) load_w8(w, w_bf16, col[j], wv[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  }
+  int parity = 0;
+  for (long long row = group; row < T; row += (long long)gridDim.x * RPB) {
+    const long long o = row * d;
+    Raw8<GT> rg[C];
+    Raw8<RT> rr[C], rd[C];
+    const float c = rstd[row];
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (live[j]) {
+        rg[j].load(du + o + col[j]);
+        rr[j].load(r + o + col[j]);
+        if (dr) rd[j].load(dr + o + col[j]);
+      }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (live[j]) {
+        float g[8], h[8];
+        rg[j].get(g);
+        rr[j].get(h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float gx = g[i] * (h[i] * c);
+          dw[j][i] += gx;
+          s = fmaf(gx, wv[j][i], s);
+        }
+      }
+    s = row_sum<TPR>(s, red, parity);
+    parity ^= 1;
+    const float m = s / (float)d;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (live[j]) {
+        float g[8], h[8], out[8];
+        rg[j].get(g);
+        rr[j].get(h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = c * (g[i] * wv[j][i] - h[i] * c * m);
+        if (dr) {
+          float t[8];
+          rd[j].get(t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) out[i] += t[i];
+        }
+        Vec8<RT>::store(dx + o + col[j], out);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (live[j]) Vec8<float>::store(part + group * d + col[j], dw[j]);
+}
+
+// dw[j] = sum over the groups of part[., j].  A block owns 64 columns; its
+// wave w adds groups w, w + 16, ... and wave 0 adds the waves' sums in order.
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part, int groups, int d,
+                                                  float* __restrict__ dw) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (col < d)
+    for (int g = wave; g < groups; g += 16) s += part[(long long)g * d + col];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < d) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    dw[col] = s;
+  }
+}
+
+// Threads a row is shared by and chunks a thread holds, by the row's length.
+struct NormShape {
+  int tpr, chunks;
+};
+NormShape norm_shape(int d) {
+  if (d <= 512) return {64, 1};
+  if (d <= 2048) return {64, 4};
+  if (d <= 8192) return {256, 4};
+  return {1024, 4};
+}
+
+int norm_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    cus = 256;
+  return cus;
+}
+
+// Blocks of the backward: each leaves one row of dw sums per row group.
+int norm_bwd_blocks(long long T, int d) {
+  const NormShape s = norm_shape(d);
+  const int rpb = s.tpr < 256 ? 256 / s.tpr : 1;
+  const long long need = ceil_div(T, rpb);
+  const long long cap = 512;
+  return (int)(need < cap ? need : cap);
+}
+
+bool is_fp(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
+
+template <typename XT, typename RT>
+void launch_norm(const void* x, const void* resid, const void* w, bool w_bf16, float eps, long long T, int d,
+                 void* r_out, void* u, bool u_bf16, uint8_t* q, float* q_scale, float* rstd, hipStream_t st) {
+  const NormShape s = norm_shape(d);
+  const int threads = s.tpr < 256 ? 256 : s.tpr, rpb = threads / s.tpr;
+  const long long need = ceil_div(T, rpb);
+  const long long cap = (long long)norm_cus() * 8;
+  const dim3 grid((unsigned)(need < cap ? need : cap));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, static_cast<const XT*>(x), static_cast<const RT*>(resid), w,
+                       w_bf16, eps, T, d, static_cast<RT*>(r_out), u, u_bf16, q, q_scale, rstd);
+  };
+  if (s.tpr == 64 && s.chunks == 1)
+    go(k_rmsnorm<XT, RT, 64, 1>);
+  else if (s.tpr == 64)
+    go(k_rmsnorm<XT, RT, 64, 4>);
+  else if (s.tpr == 256)
+    go(k_rmsnorm<XT, RT, 256, 4>);
+  else
+    go(k_rmsnorm<XT, RT, 1024, 4>);
+}
+
+template <typename GT, typename RT>
+void launch_norm_bwd(const void* du, const void* r, const void* w, bool w_bf16, const float* rstd, const void* dr,
+                     long long T, int d, void* dx, float* part, hipStream_t st) {
+  const NormShape s = norm_shape(d);
+  const int threads = s.tpr < 256 ? 256 : s.tpr;
+  const dim3 grid(norm_bwd_blocks(T, d));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, static_cast<const GT*>(du), static_cast<const RT*>(r), w,
+                       w_bf16, rstd, static_cast<const RT*>(dr), T, d, static_cast<RT*>(dx), part);
+  };
+  if (s.tpr == 64 && s.chunks == 1)
+    go(k_rmsnorm_bwd<GT, RT, 64, 1>);
+  else if (s.tpr == 64)
+    go(k_rmsnorm_bwd<GT, RT, 64, 4>);
+  else if (s.tpr == 256)
+    go(k_rmsnorm_bwd<GT, RT, 256, 4>);
+  else
+    go(k_rmsnorm_bwd<GT, RT, 1024, 4>);
+}
+
+int norm_bwd_groups(long long T, int d) {
+  const NormShape s = norm_shape(d);
+  return norm_bwd_blocks(T, d) * (s.tpr < 256 ? 256 / s.tpr : 1);
+}
+
+bool norm_d_ok(int d) { return d >= 8 && d % 8 == 0 && d <= NORM_MAX_D; }
+
+}  // namespace
+
+moe_status rmsnorm(const void* x, moe_dtype x_t, const void* resid, moe_dtype r_t, const void* w, moe_dtype w_t,
+                   float eps, long long T, int d, void* r_out, void* u, moe_dtype u_t, uint8_t* q, float* q_scale,
+                   float* rstd, void* stream) {
+  MOE_REQUIRE(is_fp(x_t) && is_fp(w_t), MOE_EINVAL, "x_t and w_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(!(resid || r_out) || is_fp(r_t), MOE_EINVAL, "r_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(!u || is_fp(u_t), MOE_EINVAL, "u_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(std::isfinite(eps) && eps >= 0.f, MOE_EINVAL, "eps must be finite and not negative");
+  MOE_REQUIRE(T >= 0 && T < (1LL << 40) && d >= 8 && d % 8 == 0, MOE_EINVAL,
+              "need T >= 0 and d a positive multiple of 8");
+  MOE_REQUIRE(d <= NORM_MAX_D, MOE_EUNSUPPORTED, "d above 32768");
+  MOE_REQUIRE((q == nullptr) == (q_scale == nullptr), MOE_EINVAL, "q and q_scale go together");
+  MOE_REQUIRE(!q || d % 128 == 0, MOE_EINVAL, "E4M3 tiles need d % 128 == 0");
+  MOE_REQUIRE(T == 0 || u || q, MOE_EINVAL, "u and q are both NULL");
+  MOE_REQUIRE(T == 0 || (x && w), MOE_EINVAL, "NULL pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(resid) && aligned16(w) && aligned16(r_out) && aligned16(u) && aligned16(q),
+              MOE_EINVAL, "x, resid, weight, r_out, u and q must be 16-byte aligned");
+  if (T == 0) return MOE_OK;
+  hipStream_t st = as_stream(stream);
+  const bool rf = !(resid || r_out) || r_t == MOE_F32;
+  auto go = [&](auto launch) {
+    launch(x, resid, w, w_t == MOE_BF16, eps, T, d, r_out, u, u_t == MOE_BF16, q, q_scale, rstd, st);
+  };
+  if (x_t == MOE_F32) {
+    if (rf) go(launch_norm<float, float>); else go(launch_norm<float, uint16_t>);
+  } else {
+    if (rf) go(launch_norm<uint16_t, float>); else go(launch_norm<uint16_t, uint16_t>);
+  }
+  return launch_status("moe_rmsnorm");
+}
+
+size_t rmsnorm_backward_workspace_bytes(long long T, int d) {
+  if (T <= 0 || !norm_d_ok(d)) return 0;
+  return (size_t)norm_bwd_groups(T, d) * d * sizeof(float);
+}
+
+moe_status rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t, const void* w, moe_dtype w_t,
+                            const float* rstd, const void* dr, long long T, int d, void* dx, float* dw, void* ws,
+                            size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(is_fp(du_t) && is_fp(r_t) && is_fp(w_t), MOE_EINVAL, "du_t, r_t and w_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(T >= 0 && T < (1LL << 40) && d >= 8 && d % 8 == 0, MOE_EINVAL,
+              "need T >= 0 and d a positive multiple of 8");
+  MOE_REQUIRE(d <= NORM_MAX_D, MOE_EUNSUPPORTED, "d above 32768");
+  MOE_REQUIRE(dw, MOE_EINVAL, "dw is NULL");
+  MOE_REQUIRE(T == 0 || (du && r && w && rstd && dx), MOE_EINVAL, "NULL pointer");
+  MOE_REQUIRE(aligned16(du) && aligned16(r) && aligned16(w) && aligned16(dr) && aligned16(dx) && aligned16(ws),
+              MOE_EINVAL, "du, r, weight, dr, dx and ws must be 16-byte aligned");
+  MOE_REQUIRE(T == 0 || (ws && ws_bytes >= rmsnorm_backward_workspace_bytes(T, d)), MOE_EWORKSPACE,
+              "workspace smaller than moe_rmsnorm_backward_workspace_bytes");
+  hipStream_t st = as_stream(stream);
+  float* part = static_cast<float*>(ws);
+  if (T > 0) {
+    auto go = [&](auto launch) { launch(du, r, w, w_t == MOE_BF16, rstd, dr, T, d, dx, part, st); };
+    if (du_t == MOE_F32) {
+      if (r_t == MOE_F32) go(launch_norm_bwd<float, float>); else go(launch_norm_bwd<float, uint16_t>);
+    } else {
+      if (r_t == MOE_F32) go(launch_norm_bwd<uint16_t, float>); else go(launch_norm_bwd<uint16_t, uint16_t>);
+    }
+  }
+  // T == 0: no groups, dw = 0
+  hipLaunchKernelGGL(k_norm_dw, dim3((d + 63) / 64), dim3(1024), 0, st, part, T > 0 ? norm_bwd_groups(T, d) : 0, d, dw);
+  return launch_status("moe_rmsnorm_backward");
+}
+
+}  // namespace moe
