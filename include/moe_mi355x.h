@@ -61,6 +61,7 @@ extern "C" {
 #define MOE_MAX_K 16           /* routed experts per token */
 #define MOE_TILE_ROWS 256      /* rows per entry of the GEMM tile map */
 #define MOE_NORM_MAX_D 32768   /* columns of moe_rmsnorm */
+#define MOE_FEW_TOKENS 32      /* tokens of moe_layer_few */
 
 typedef enum {
   MOE_OK = 0,
@@ -73,7 +74,8 @@ typedef enum {
 typedef enum {
   MOE_F32 = 0,
   MOE_BF16 = 1,
-  MOE_E4M3 = 2
+  MOE_E4M3 = 2,
+  MOE_E2M1 = 3 /* two codes per byte, an exponent byte per 32 columns (fp4_*) */
 } moe_dtype;
 
 /* Flags of moe_combine: drop a term of the combine equation (component checks). */
@@ -603,6 +605,89 @@ moe_status moe_rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, m
                                 const void* weight, moe_dtype w_t, const float* rstd,
                                 const void* dr, long long T, int d, void* dx, float* dw,
                                 void* ws, size_t ws_bytes, void* stream);
+
+/* ========================================================================
+ * 4-bit weights.  A value is an E2M1 code (sign, two exponent bits with bias
+ * 1, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times
+ * 2^(b - 127), b a byte that 32 consecutive columns of a row share (b = 255:
+ * NaN).  Two codes to a byte, the even column in the low half; rows of q are
+ * cols / 2 bytes, rows of scale cols / 32 bytes.
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * fp4_quantize_groups: per group of 32 the smallest 2^k (k >= -126) with
+ * amax <= 6 * 2^k (k = 0 for a group of zeros), b = k + 127, and code =
+ * round-to-nearest-even(x / 2^k): the rule of fp8_quantize_tiles for this
+ * format; finite input never saturates.
+ *   x, x_t   device [rows, cols], MOE_F32 or MOE_BF16
+ *   q        device [rows, cols / 2] uint8 out; scale device [rows, cols / 32]
+ *            uint8 out
+ *   Errors: MOE_EINVAL for NULL pointers, bad sizes (cols % 32 != 0), x_t.
+ * fp4_dequantize_groups: the values, exact in fp32 and in bf16 (for b <= 252).
+ * ---------------------------------------------------------------------- */
+moe_status fp4_quantize_groups(const void* x, moe_dtype x_t, long long rows, long long cols,
+                               uint8_t* q, uint8_t* scale, void* stream);
+moe_status fp4_dequantize_groups(const uint8_t* q, const uint8_t* scale, long long rows,
+                                 long long cols, void* out, moe_dtype out_t, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fp4_matvec: products of a 4-bit weight matrix with a few token rows,
+ *   y[t, n] = sum_k x[t, k] W[n, k],  W the values of (q, scale)
+ * (fp32 sums in a fixed order, one rounding to y_t).  Made for few tokens,
+ * where reading W bounds it; any T is computed, W being read again for every
+ * 32 tokens.
+ *   x, x_t   device [T, K], MOE_BF16
+ *   q, scale device [N, K / 2], [N, K / 32] uint8
+ *   y, y_t   device [T, N] out, MOE_F32 or MOE_BF16 (element alignment)
+ *   ws       device, fp4_matvec_workspace_bytes(T, N, K) bytes (may be NULL
+ *            when that is 0)
+ *   Errors: MOE_EINVAL for NULL pointers, bad sizes (K < 32, K % 32 != 0) or
+ *   types; MOE_EUNSUPPORTED for fp32 x, K above 2^20, T above 1048560, N
+ *   above 2^34; MOE_EWORKSPACE for a small ws.  T == 0 or N == 0 is valid.
+ * ---------------------------------------------------------------------- */
+size_t fp4_matvec_workspace_bytes(int T, long long N, int K);
+moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T,
+                      long long N, int K, void* y, moe_dtype y_t, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_layer_few: the whole layer forward for at most MOE_FEW_TOKENS tokens
+ * in one call (a decode step of a few sequences, or a few drafted tokens):
+ * the routing of moe_route, the FFNs of moe_expert_gemm and the sum of
+ * moe_combine, reading each touched expert's weights once.
+ *   u, u_t       device [T, d], MOE_F32 or MOE_BF16
+ *   centroids, bias: as moe_route
+ *   w_t, w13, w13_scale, w2, w2_scale: as moe_expert_gemm for MOE_F32,
+ *                MOE_BF16 and MOE_E4M3 (fp32 block scales); MOE_E2M1: codes
+ *                [Nr+Ns, 2I, d/2] and [Nr+Ns, d, I/2] with exponent bytes
+ *                [Nr+Ns, 2I, d/32] and [Nr+Ns, d, I/32] (fp4_quantize_groups)
+ *   resid, r_t   device [T, d], MOE_F32 or MOE_BF16, added to the output: u
+ *                for the combine equation, the stream r of moe_rmsnorm for a
+ *                pre-norm block; NULL adds nothing
+ *   topk_idx, topk_gate, topk_score (may be NULL), expert_load (may be NULL):
+ *                out, as moe_route
+ *   ws           device, moe_layer_few_workspace_bytes(...) bytes
+ *   out, out_t   device [T, d] out, MOE_F32 or MOE_BF16; may be u or resid of
+ *                the same type
+ * Supported (u_t, w_t): (F32, F32), and BF16 with BF16, E4M3 or E2M1.  Every
+ * sum is fp32 in a fixed order, so results are bitwise reproducible; with
+ * bf16 tokens h is rounded to bf16 (the operand of the down projection), y is
+ * not rounded.
+ *   Errors: MOE_EINVAL for NULL pointers, bad types or sizes (d or I not a
+ *   multiple of 8, K, Nr, Ns as moe_route and moe_permute); MOE_EUNSUPPORTED
+ *   for T > MOE_FEW_TOKENS, other type pairs, E4M3 with d or I not a multiple
+ *   of 128, E2M1 with d or I not a multiple of 32, an expert's matrix, the
+ *   centroids or h of 2 GiB or more; MOE_EWORKSPACE for a small ws.  T == 0 is
+ *   valid: expert_load is zeroed.
+ * ---------------------------------------------------------------------- */
+size_t moe_layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t);
+moe_status moe_layer_few(const void* u, moe_dtype u_t, const float* centroids, const float* bias,
+                         moe_dtype w_t, const void* w13, const void* w13_scale,
+                         const void* w2, const void* w2_scale,
+                         int T, int d, int Nr, int Ns, int I, int K,
+                         const void* resid, moe_dtype r_t,
+                         int32_t* topk_idx, float* topk_gate, float* topk_score, int32_t* expert_load,
+                         void* ws, size_t ws_bytes, void* out, moe_dtype out_t, void* stream);
 
 #ifdef __cplusplus
 }

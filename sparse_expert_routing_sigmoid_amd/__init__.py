@@ -20,12 +20,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = range(5)
-MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_E2M1 = 0, 1, 2, 3
 MOE_COMBINE_NO_RESIDUAL, MOE_COMBINE_NO_SHARED, MOE_COMBINE_NO_ROUTED = 1, 2, 4
 MOE_TILE_ROWS = 256
 MOE_MAX_K = 16
 MOE_MAX_EXPERTS = 1024
 MOE_NORM_MAX_D = 32768
+MOE_FEW_TOKENS = 32
 
 # Every symbol the header declares, with its ctypes signature.
 _vp, _i, _ll, _sz, _f, _u = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float, ctypes.c_uint
@@ -68,6 +69,13 @@ SIGNATURES = {
     "moe_rmsnorm": (_i, [_vp, _i, _vp, _i, _vp, _i, _f, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp]),
     "moe_rmsnorm_backward_workspace_bytes": (_sz, [_ll, _i]),
     "moe_rmsnorm_backward": (_i, [_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _ll, _i, _vp, _vp, _vp, _sz, _vp]),
+    "fp4_quantize_groups": (_i, [_vp, _i, _ll, _ll, _vp, _vp, _vp]),
+    "fp4_dequantize_groups": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _vp]),
+    "fp4_matvec_workspace_bytes": (_sz, [_i, _ll, _i]),
+    "fp4_matvec": (_i, [_vp, _i, _vp, _vp, _i, _ll, _i, _vp, _i, _vp, _sz, _vp]),
+    "moe_layer_few_workspace_bytes": (_sz, [_i] * 7),
+    "moe_layer_few": (_i, [_vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp] + [_i] * 6 + [_vp, _i] + [_vp] * 5 +
+                      [_sz, _vp, _i, _vp]),
 }
 
 _lib = None
@@ -394,11 +402,63 @@ def moe_rmsnorm_backward(du, r, weight, rstd, dr, dx, dw, ws, stream=None):
                                       _nbytes(ws), _stream(stream)))
 
 
+def fp4_quantize_groups(x, q, scale, stream=None):
+    """E2M1 codes q [..., cols / 2] (uint8, two to a byte) and exponent bytes
+    scale [..., cols / 32] of x [..., cols], one power of two per 32 columns."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    _shape(q, (*x.shape[:-1], cols // 2), torch.uint8, "q")
+    _shape(scale, (*x.shape[:-1], cols // 32), torch.uint8, "scale")
+    _check(lib().fp4_quantize_groups(_ptr(x), dtype_code(x), rows, cols, _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def fp4_dequantize_groups(q, scale, out, stream=None):
+    """Values of E2M1 groups into out [..., cols] (fp32 or bf16)."""
+    cols = out.shape[-1]
+    rows = out.numel() // cols if cols else 0
+    _shape(q, (*out.shape[:-1], cols // 2), torch.uint8, "q")
+    _shape(scale, (*out.shape[:-1], cols // 32), torch.uint8, "scale")
+    _check(lib().fp4_dequantize_groups(_ptr(q), _ptr(scale), rows, cols, _ptr(out), dtype_code(out), _stream(stream)))
+
+
+def fp4_matvec_workspace_bytes(T, N, K):
+    return lib().fp4_matvec_workspace_bytes(T, N, K)
+
+
+def fp4_matvec(x, q, scale, y, ws=None, stream=None):
+    """y [T, N] = x [T, K] W^T with the 4-bit W [N, K] of (q, scale)."""
+    T, K = x.shape
+    N = q.shape[0]
+    _shape(q, (N, K // 2), torch.uint8, "q")
+    _shape(scale, (N, K // 32), torch.uint8, "scale")
+    _shape(y, (T, N), y.dtype, "y")
+    _check(lib().fp4_matvec(_ptr(x), dtype_code(x), _ptr(q), _ptr(scale), T, N, K, _ptr(y), dtype_code(y), _ptr(ws),
+                            _nbytes(ws), _stream(stream)))
+
+
+def moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t):
+    return lib().moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t)
+
+
+def moe_layer_few(u, centroids, bias, w: "ExpertWeights", Ns, I, K, resid, topk_idx, topk_gate, topk_score, expert_load,
+                  ws, out, stream=None):
+    """The whole layer for up to MOE_FEW_TOKENS tokens u [T, d]; resid [T, d]
+    or None is added to out [T, d]."""
+    T, d = u.shape
+    Nr = centroids.shape[0]
+    _check(lib().moe_layer_few(_ptr(u), dtype_code(u), _ptr(centroids), _ptr(bias), w.w_t, _ptr(w.w13),
+                               _ptr(w.w13_scale), _ptr(w.w2), _ptr(w.w2_scale), T, d, Nr, Ns, I, K, _ptr(resid),
+                               MOE_F32 if resid is None else dtype_code(resid), _ptr(topk_idx), _ptr(topk_gate),
+                               _ptr(topk_score), _ptr(expert_load), _ptr(ws), _nbytes(ws), _ptr(out), dtype_code(out),
+                               _stream(stream)))
+
+
 # ------------------------------------------------------- layer plumbing --
 @dataclass
 class ExpertWeights:
     """Expert weights as the library reads them: W13 [E, 2I, d], W2 [E, d, I]
-    (bf16/fp32 tensors, or E4M3 codes (uint8) with fp32 block scales)."""
+    (bf16/fp32 tensors, E4M3 codes (uint8) with fp32 block scales, or E2M1
+    codes two to a byte (uint8) with an exponent byte (uint8) per 32 columns)."""
     w_t: int
     w13: torch.Tensor
     w2: torch.Tensor
@@ -418,6 +478,80 @@ def quantize_weights(w13: torch.Tensor, w2: torch.Tensor, stream=None) -> Expert
     fp8_quantize_tiles(w13, 128, q13, s13, stream=stream)
     fp8_quantize_tiles(w2, 128, q2, s2, stream=stream)
     return ExpertWeights(MOE_E4M3, q13, q2, s13, s2)
+
+
+def quantize_weights_fp4(w13: torch.Tensor, w2: torch.Tensor, stream=None) -> ExpertWeights:
+    """E2M1 codes and exponent bytes of fp32/bf16 expert weights, made by
+    fp4_quantize_groups (for FewTokenLayer)."""
+    def one(w):
+        q = torch.empty((*w.shape[:-1], w.shape[-1] // 2), dtype=torch.uint8, device=w.device)
+        s = torch.empty((*w.shape[:-1], w.shape[-1] // 32), dtype=torch.uint8, device=w.device)
+        fp4_quantize_groups(w, q, s, stream)
+        return q, s
+
+    (q13, s13), (q2, s2) = one(w13), one(w2)
+    return ExpertWeights(MOE_E2M1, q13, q2, s13, s2)
+
+
+class FewTokenLayer:
+    """One DeepSeekMoE layer forward for at most T <= MOE_FEW_TOKENS tokens
+    (moe_layer_few): the serving form of MoeLayer for a few sequences or
+    drafted tokens, with fp32, bf16, E4M3 or E2M1 expert weights.
+
+    Holds the outputs and the workspace; calls on it must not overlap.  After
+    forward() of n tokens, the first n rows of topk_idx, topk_gate, topk_score
+    and out, and expert_load, are those of the call."""
+
+    def __init__(self, T, d, Nr, Ns, I, K, act_dtype, weights: ExpertWeights, out_dtype=None, device="cuda"):
+        self.T, self.d, self.Nr, self.Ns, self.I, self.K = T, d, Nr, Ns, I, K
+        self.act_dtype, self.w = act_dtype, weights
+        if not 0 <= T <= MOE_FEW_TOKENS:
+            raise ValueError(f"T: at most {MOE_FEW_TOKENS} tokens")
+        E = Nr + Ns
+        per_byte = 2 if weights.w_t == MOE_E2M1 else 1
+        store = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_E4M3: torch.uint8,
+                 MOE_E2M1: torch.uint8}[weights.w_t]
+        _shape(weights.w13, (E, 2 * I, d // per_byte), store, "w13")
+        _shape(weights.w2, (E, d, I // per_byte), store, "w2")
+        if weights.w_t in (MOE_E4M3, MOE_E2M1) and (weights.w13_scale is None or weights.w2_scale is None):
+            raise ValueError("E4M3 and E2M1 weights need scales")
+        if weights.w_t == MOE_E4M3:
+            _shape(weights.w13_scale, (E, 2 * I // 128, d // 128), torch.float32, "w13_scale")
+            _shape(weights.w2_scale, (E, d // 128, I // 128), torch.float32, "w2_scale")
+        if weights.w_t == MOE_E2M1:
+            _shape(weights.w13_scale, (E, 2 * I, d // 32), torch.uint8, "w13_scale")
+            _shape(weights.w2_scale, (E, d, I // 32), torch.uint8, "w2_scale")
+        dev = torch.device(device)
+        self.topk_idx = torch.empty((T, K), dtype=torch.int32, device=dev)
+        self.topk_gate = torch.empty((T, K), dtype=torch.float32, device=dev)
+        self.topk_score = torch.empty((T, K), dtype=torch.float32, device=dev)
+        self.expert_load = torch.empty((Nr,), dtype=torch.int32, device=dev)
+        self.out = torch.empty((T, d), dtype=act_dtype if out_dtype is None else out_dtype, device=dev)
+        u_t = MOE_BF16 if act_dtype == torch.bfloat16 else MOE_F32
+        self.ws = torch.empty((max(moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t), 1),), dtype=torch.uint8,
+                              device=dev)
+
+    def forward(self, u, centroids, bias, residual=None, flags=0, stream=None):
+        """out [n, d] = residual + the experts' part for u [n, d], n <= T.
+        residual None is u, as in the combine equation (a pre-norm block
+        passes its stream); MOE_COMBINE_NO_RESIDUAL in flags adds nothing."""
+        n = u.shape[0]
+        if n > self.T or u.shape[1] != self.d or u.dtype != self.act_dtype:
+            raise ValueError(f"u: expected at most [{self.T}, {self.d}] {self.act_dtype}, got {tuple(u.shape)} {u.dtype}")
+        if flags & ~MOE_COMBINE_NO_RESIDUAL:
+            raise ValueError("flags: only MOE_COMBINE_NO_RESIDUAL")
+        _same(residual, u, "residual")
+        _shape(centroids, (self.Nr, self.d), torch.float32, "centroids")
+        _shape(bias, (self.Nr,), torch.float32, "bias")
+        resid = None if flags else u if residual is None else residual
+        out = self.out if n == self.T else self.out[:n]
+        moe_layer_few(u, centroids, bias, self.w, self.Ns, self.I, self.K, resid, self.topk_idx, self.topk_gate,
+                      self.topk_score, self.expert_load, self.ws, out, stream)
+        return out
+
+    def update_bias(self, bias, tokens=None, gamma=0.001, stream=None):
+        """End-of-step bias rule for the loads of the last forward() of `tokens` tokens (T by default)."""
+        moe_bias_update(self.expert_load, (self.T if tokens is None else tokens) * self.K, gamma, bias, stream)
 
 
 class MoeLayer:

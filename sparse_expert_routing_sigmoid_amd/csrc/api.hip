@@ -93,6 +93,19 @@ size_t rmsnorm_backward_workspace_bytes(long long T, int d);
 moe_status rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t, const void* w, moe_dtype w_t,
                             const float* rstd, const void* dr, long long T, int d, void* dx, float* dw, void* ws,
                             size_t ws_bytes, void* stream);
+moe_status fp4_quantize(const void* x, moe_dtype x_t, long long rows, long long cols, uint8_t* q, uint8_t* scale,
+                        void* stream);
+moe_status fp4_dequantize(const uint8_t* q, const uint8_t* scale, long long rows, long long cols, void* out,
+                          moe_dtype out_t, void* stream);
+size_t fp4_matvec_workspace_bytes(int T, long long N, int K);
+moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
+                      void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream);
+size_t layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t);
+moe_status layer_few(const void* u, moe_dtype u_t, const float* centroids, const float* bias, moe_dtype w_t,
+                     const void* w13, const void* w13_scale, const void* w2, const void* w2_scale, int T, int d, int Nr,
+                     int Ns, int I, int K, const void* resid, moe_dtype r_t, int32_t* topk_idx, float* topk_gate,
+                     float* topk_score, int32_t* expert_load, void* ws, size_t ws_bytes, void* out, moe_dtype out_t,
+                     void* stream);
 
 namespace {
 thread_local std::string g_last_error;
@@ -341,6 +354,40 @@ moe_status moe_rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, m
                                 float* dw, void* ws, size_t ws_bytes, void* stream) {
   moe::clear_error();
   return moe::rmsnorm_backward(du, du_t, r, r_t, weight, w_t, rstd, dr, T, d, dx, dw, ws, ws_bytes, stream);
+}
+
+moe_status fp4_quantize_groups(const void* x, moe_dtype x_t, long long rows, long long cols, uint8_t* q,
+                               uint8_t* scale, void* stream) {
+  moe::clear_error();
+  return moe::fp4_quantize(x, x_t, rows, cols, q, scale, stream);
+}
+
+moe_status fp4_dequantize_groups(const uint8_t* q, const uint8_t* scale, long long rows, long long cols, void* out,
+                                 moe_dtype out_t, void* stream) {
+  moe::clear_error();
+  return moe::fp4_dequantize(q, scale, rows, cols, out, out_t, stream);
+}
+
+size_t fp4_matvec_workspace_bytes(int T, long long N, int K) { return moe::fp4_matvec_workspace_bytes(T, N, K); }
+
+moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
+                      void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream) {
+  moe::clear_error();
+  return moe::fp4_matvec(x, x_t, q, scale, T, N, K, y, y_t, ws, ws_bytes, stream);
+}
+
+size_t moe_layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t) {
+  return moe::layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t);
+}
+
+moe_status moe_layer_few(const void* u, moe_dtype u_t, const float* centroids, const float* bias, moe_dtype w_t,
+                         const void* w13, const void* w13_scale, const void* w2, const void* w2_scale, int T, int d,
+                         int Nr, int Ns, int I, int K, const void* resid, moe_dtype r_t, int32_t* topk_idx,
+                         float* topk_gate, float* topk_score, int32_t* expert_load, void* ws, size_t ws_bytes,
+                         void* out, moe_dtype out_t, void* stream) {
+  moe::clear_error();
+  return moe::layer_few(u, u_t, centroids, bias, w_t, w13, w13_scale, w2, w2_scale, T, d, Nr, Ns, I, K, resid, r_t,
+                        topk_idx, topk_gate, topk_score, expert_load, ws, ws_bytes, out, out_t, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,196 @@
+// 4-bit weights: E2M1 codes with one power-of-two scale per 32 columns of a
+// row (the group size and the element and scale formats of the OCP
+// Microscaling specification's 4-bit format), their quantiser, and products
+// with a few token rows.
+#include "skinny.h"
+#include "vec8.h"
+
+namespace moe {
+
+namespace {
+
+// Smallest 2^k (k >= -126) with amax <= 6 * 2^k, or k = 0 for amax == 0: with
+// amax = 1.M * 2^E, k = E - 2 when 1.M <= 1.5, else E - 1.
+__device__ __forceinline__ int e2m1_scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax) & 0x7FFFFFFFu;
+  if (b == 0) return 0;
+  const int E = (int)(b >> 23) - 127;
+  if (E == -127) return -126;  // subnormal amax
+  const int k = (b & 0x7FFFFFu) <= 0x400000u ? E - 2 : E - 1;
+  return k < -126 ? -126 : k;
+}
+
+// Code of v (|v| <= 6): magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 are codes 0 to 7,
+// bit 3 is the sign; round to nearest, a tie to the even code.
+__device__ __forceinline__ uint32_t e2m1_code(float v) {
+  const float a = fabsf(v);
+  const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
+  return c | (__float_as_uint(v) >> 31) << 3;
+}
+
+// Eight values per thread; four threads hold a group of 32.
+template <typename XT>
+__global__ __launch_bounds__(256) void k_fp4_quant(const XT* __restrict__ x, long long chunks, uint8_t* __restrict__ q,
+                                                   uint8_t* __restrict__ scale) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // chunks % 4 == 0: a group is live or not as one
+  if (i >= chunks) return;
+  float v[8];
+  Vec8<XT>::load(x + i * 8, v);
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
+  amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
+  const int k = e2m1_scale_exp(amax);
+  const float inv = exp2_int(-k);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w |= e2m1_code(v[j] * inv) << (4 * j);
+  *reinterpret_cast<uint32_t*>(q + i * 4) = w;
+  if ((i & 3) == 0) scale[i >> 2] = (uint8_t)(k + 127);
+}
+
+template <typename OT>
+__global__ __launch_bounds__(256) void k_fp4_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                                                     long long chunks, OT* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i * 4);
+  const float sc = __uint_as_float((uint32_t)scale[i >> 2] << 23);
+  float v[8];
+  auto put = [&](sk_bf16x2 p, int j) {  // exact: one significant bit beside the leading one
+    v[j] = static_cast<float>(p[0]);
+    v[j + 1] = static_cast<float>(p[1]);
+  };
+  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0), 0);
+  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1), 2);
+  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2), 4);
+  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3), 6);
+  Vec8<OT>::store(out + i * 8, v);
+}
+
+// One block: RT 16-row tiles of W and up to 16 NT tokens.
+constexpr int MV_W = 8;  // waves
+
+template <int RT, int NT, typename OT>
+__global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                                                          const uint8_t* __restrict__ scale, int T, long long N, int K,
+                                                          OT* __restrict__ y) {
+  using S = Skinny<MOE_E2M1, uint16_t, RT, NT>;
+  __shared__ sk_f32x4 red[MV_W * RT * NT * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long row0 = (long long)blockIdx.x * (16 * RT);
+  const int rows = (int)(N - row0 < 16 * RT ? N - row0 : 16 * RT);
+  const int t0 = blockIdx.y * (16 * NT);
+  const int toks = T - t0 < 16 * NT ? T - t0 : 16 * NT;
+  typename S::Lanes L;
+  L.K = K;
+  L.g = lane >> 4;
+  L.rw = sk_rsrc(q + row0 * (K / 2), (uint32_t)rows * (uint32_t)(K / 2));
+  L.rs = sk_rsrc(scale + row0 * (K / 32), (uint32_t)rows * (uint32_t)(K / 32));
+  L.rx = sk_rsrc(x + (long long)t0 * K, (uint32_t)toks * (uint32_t)K * 2u);
+#pragma unroll
+  for (int f = 0; f < RT; ++f) {
+    const int r = f * 16 + (lane & 15);
+    L.w_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 2) + L.g * 16u : SK_OOB;
+    L.s_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 32) + L.g : SK_OOB;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = n * 16 + (lane & 15);
+    L.x_off[n] = t < toks ? (uint32_t)t * (uint32_t)K * 2u + L.g * (uint32_t)S::XBYTES : SK_OOB;
+  }
+  sk_f32x4 acc[RT][NT];
+  S::template run<2>(acc, L, wave, (K + S::STEP - 1) / S::STEP, MV_W);
+  sk_put<RT, NT>(red, acc);
+  for (int e = threadIdx.x; e < RT * NT * 64; e += 64 * MV_W) {
+    const int l = e & 63, n = (e >> 6) % NT, f = (e >> 6) / NT;
+    const int t = n * 16 + (l & 15), r = f * 16 + 4 * (l >> 4);
+    if (t >= toks || r >= rows) continue;
+    const sk_f32x4 s = sk_get<MV_W, RT, NT>(red, f, n, l);
+    OT* o = y + (long long)(t0 + t) * N + row0 + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + i < rows) {
+        if constexpr (sizeof(OT) == 2)
+          o[i] = f32_to_bf16(s[i]);
+        else
+          o[i] = s[i];
+      }
+  }
+}
+
+constexpr int MV_MAX_K = 1 << 20;  // 64 rows and 32 tokens of it stay within 32-bit offsets
+
+}  // namespace
+
+moe_status fp4_quantize(const void* x, moe_dtype x_t, long long rows, long long cols, uint8_t* q, uint8_t* scale,
+                        void* stream) {
+  MOE_REQUIRE(x_t == MOE_F32 || x_t == MOE_BF16, MOE_EINVAL, "x_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(rows >= 0 && cols >= 0 && cols % 32 == 0, MOE_EINVAL, "cols must be a multiple of 32");
+  MOE_REQUIRE(rows == 0 || cols == 0 || (x && q && scale), MOE_EINVAL, "NULL pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(q), MOE_EINVAL, "x and q must be 16-byte aligned");
+  MOE_REQUIRE(rows == 0 || cols <= (1LL << 40) / rows, MOE_EINVAL, "too many values");
+  const long long chunks = rows * (cols / 8);
+  if (chunks == 0) return MOE_OK;
+  hipStream_t st = as_stream(stream);
+  const dim3 grid((unsigned)ceil_div(chunks, 256));
+  if (x_t == MOE_F32)
+    hipLaunchKernelGGL(k_fp4_quant<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), chunks, q, scale);
+  else
+    hipLaunchKernelGGL(k_fp4_quant<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(x), chunks, q, scale);
+  return launch_status("fp4_quantize_groups");
+}
+
+moe_status fp4_dequantize(const uint8_t* q, const uint8_t* scale, long long rows, long long cols, void* out,
+                          moe_dtype out_t, void* stream) {
+  MOE_REQUIRE(out_t == MOE_F32 || out_t == MOE_BF16, MOE_EINVAL, "out_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(rows >= 0 && cols >= 0 && cols % 32 == 0, MOE_EINVAL, "cols must be a multiple of 32");
+  MOE_REQUIRE(rows == 0 || cols == 0 || (q && scale && out), MOE_EINVAL, "NULL pointer");
+  MOE_REQUIRE(aligned16(q) && aligned16(out), MOE_EINVAL, "q and out must be 16-byte aligned");
+  MOE_REQUIRE(rows == 0 || cols <= (1LL << 40) / rows, MOE_EINVAL, "too many values");
+  const long long chunks = rows * (cols / 8);
+  if (chunks == 0) return MOE_OK;
+  hipStream_t st = as_stream(stream);
+  const dim3 grid((unsigned)ceil_div(chunks, 256));
+  if (out_t == MOE_F32)
+    hipLaunchKernelGGL(k_fp4_dequant<float>, grid, dim3(256), 0, st, q, scale, chunks, static_cast<float*>(out));
+  else
+    hipLaunchKernelGGL(k_fp4_dequant<uint16_t>, grid, dim3(256), 0, st, q, scale, chunks, static_cast<uint16_t*>(out));
+  return launch_status("fp4_dequantize_groups");
+}
+
+size_t fp4_matvec_workspace_bytes(int T, long long N, int K) { return 0; }
+
+moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
+                      void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(x_t == MOE_F32 || x_t == MOE_BF16, MOE_EINVAL, "x_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(y_t == MOE_F32 || y_t == MOE_BF16, MOE_EINVAL, "y_t must be MOE_F32 or MOE_BF16");
+  MOE_REQUIRE(x_t == MOE_BF16, MOE_EUNSUPPORTED, "x must be bf16");
+  MOE_REQUIRE(T >= 0 && N >= 0 && K >= 32 && K % 32 == 0, MOE_EINVAL,
+              "need T, N >= 0 and K a positive multiple of 32");
+  MOE_REQUIRE(K <= MV_MAX_K, MOE_EUNSUPPORTED, "K above 1048576");
+  MOE_REQUIRE(T <= 16 * 65535 && N <= (1LL << 34), MOE_EUNSUPPORTED, "T above 1048560 or N above 2^34");
+  if (T == 0 || N == 0) return MOE_OK;
+  MOE_REQUIRE(x && q && scale && y, MOE_EINVAL, "NULL pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(q), MOE_EINVAL, "x and q must be 16-byte aligned");
+  MOE_REQUIRE(ws_bytes >= fp4_matvec_workspace_bytes(T, N, K), MOE_EWORKSPACE,
+              "workspace smaller than fp4_matvec_workspace_bytes");
+  hipStream_t st = as_stream(stream);
+  auto go = [&](auto kernel, int rt, int nt, auto* out) {
+    const dim3 grid((unsigned)ceil_div(N, 16 * rt), (unsigned)ceil_div(T, 16 * nt));
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * MV_W), 0, st, static_cast<const uint16_t*>(x), q, scale, T, N, K, out);
+  };
+  auto pick = [&](auto* out) {
+    using OT = std::remove_pointer_t<decltype(out)>;
+    if (N >= 16384) {
+      if (T <= 16) go(k_fp4_matvec<4, 1, OT>, 4, 1, out); else go(k_fp4_matvec<4, 2, OT>, 4, 2, out);
+    } else {
+      if (T <= 16) go(k_fp4_matvec<1, 1, OT>, 1, 1, out); else go(k_fp4_matvec<1, 2, OT>, 1, 2, out);
+    }
+  };
+  if (y_t == MOE_BF16) pick(static_cast<uint16_t*>(y)); else pick(static_cast<float*>(y));
+  return launch_status("fp4_matvec");
+}
+
+}  // namespace moe
