@@ -24,16 +24,18 @@ namespace moe {
 namespace {
 
 constexpr int FEW_T = MOE_FEW_TOKENS;
-constexpr int FEW_W = 8;    // waves of a product block
-constexpr int FEW_RT = 4;   // 16-row tiles of a product block
-constexpr int LOGIT_W = 4;  // waves of a router block
+constexpr int FEW_W = 4;    // waves of a product block
+constexpr int FEW_RT = 2;   // 16-row tiles of a product block
+constexpr int FEW_D = 2;    // steps a product wave's loads run ahead
+constexpr int LOGIT_W = 8;  // waves of a router block
+constexpr int LOGIT_PARTS = 8;
 
 // Touched routed experts, in ascending order, and the tokens of each.
 struct FewLists {
   int32_t* n;       // [1] touched routed experts
   int32_t* expert;  // [Nr]
   int32_t* tokens;  // [Nr] tokens of the expert
-  int32_t* pair;    // [Nr, FEW_T] t << 8 | k of the expert's tokens, ascending
+  int32_t* pair;    // [Nr, FEW_T] t << 16 | k of the expert's tokens, ascending
 };
 
 struct FewWs {
@@ -44,13 +46,15 @@ struct FewWs {
   size_t bytes;
 };
 
-// K axis parts of the router: enough blocks to occupy the chip, at least two
-// steps for every wave.
+// K axis parts of the router: enough blocks to occupy the chip, at least one
+// step for every wave, and few enough that the selection can have all of a
+// token's partial logits in flight at once.
 int few_parts(int d, int Nr) {
   const int step = 4 * SkinnyWeight<MOE_F32>::EPL * SkinnyWeight<MOE_F32>::LD;
   const int tiles = (Nr + 15) / 16, steps = (d + step - 1) / step;
-  const int want = 512 / tiles, most = steps / (2 * LOGIT_W);
-  const int parts = want < most ? want : most;
+  int parts = 256 / tiles;
+  if (parts > LOGIT_PARTS) parts = LOGIT_PARTS;
+  if (parts > steps / LOGIT_W) parts = steps / LOGIT_W;
   return parts < 1 ? 1 : parts;
 }
 
@@ -135,22 +139,35 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
                                                 float* __restrict__ topk_gate, float* __restrict__ topk_score,
                                                 uint32_t* mask) {
   const int lane = threadIdx.x & 63;
-  float s[EPL] = {};
+  float s[EPL];
   uint32_t key[EPL];
   uint32_t avail = 0;
-  const float* zt = z + (long long)t * Nr + lane;
-  // the parts in ascending order; EPL x 4 (EPL 16: x 1) loads in flight
-#pragma unroll(EPL > 4 ? 1 : 4)
-  for (int p = 0; p < parts; ++p, zt += (long long)T * Nr)
+  // partial logits, added in ascending order of the parts; read without
+  // branches (past Nr: expert Nr - 1), so their latencies overlap
+  constexpr int AHEAD = EPL > 4 ? 1 : LOGIT_PARTS;
+  int at[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (lane + 64 * j < Nr) s[j] += zt[64 * j];
+  for (int j = 0; j < EPL; ++j) {
+    s[j] = 0.f;
+    at[j] = t * Nr + (lane + 64 * j < Nr ? lane + 64 * j : Nr - 1);
+  }
+  for (int p0 = 0; p0 < parts; p0 += AHEAD) {
+    float v[AHEAD][EPL];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) v[q][j] = z[(p0 + q < parts ? p0 + q : p0) * T * Nr + at[j]];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] += p0 + q < parts ? v[q][j] : 0.f;
+  }
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int i = lane + 64 * j;
     key[j] = 0;
+    s[j] = 1.0f / (1.0f + expf(-s[j]));
     if (i < Nr) {
-      s[j] = 1.0f / (1.0f + expf(-s[j]));
       key[j] = float_order_key(s[j] + bias[i]);
       avail |= 1u << j;
     }
@@ -224,7 +241,7 @@ __global__ __launch_bounds__(1024) void k_few_select(const float* __restrict__ z
   __syncthreads();
   for (int i = threadIdx.x; i < T * K; i += 1024) {
     const int t = i / K, k = i % K, ex = topk_idx[i];
-    lists.pair[place[ex] * FEW_T + __popc(mask[ex] & ((1u << t) - 1))] = t << 8 | k;
+    lists.pair[place[ex] * FEW_T + __popc(mask[ex] & ((1u << t) - 1))] = t << 16 | k;
   }
   if (load)
     for (int i = threadIdx.x; i < Nr; i += 1024) load[i] = __popc(mask[i]);
@@ -245,24 +262,15 @@ struct FewArgs {
   int T, K, Nr, Ns, Nd, Kd;
 };
 
-// One item: 64 weight rows of one expert (gate/up: 32 gate rows and the up
-// rows of the same columns of h) on all of the expert's tokens.
-template <int WT, typename XT, bool GATE_UP, int NT>
-__device__ __forceinline__ void few_item(const FewArgs& A, int ex, int listed, int toks, int col0, sk_f32x4* red) {
+// One item: 16 RT weight rows of one expert (gate/up: 8 RT gate rows and the
+// up rows of the same columns of h) on up to 16 of its tokens, j0 and on.
+template <int WT, typename XT, bool GATE_UP>
+__device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, int j0, int p, int col0, sk_f32x4* red) {
   constexpr int RT = FEW_RT;
-  using S = Skinny<WT, XT, RT, NT>;
+  using S = Skinny<WT, XT, RT, 1>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int R = A.K + A.Ns;  // h and y rows of a token
-  // h row of the expert's j-th token, and that token
-  auto pair = [&](int j, int& t) {
-    if (listed < 0) {
-      t = j;
-      return j * R + A.K + (ex - A.Nr);
-    }
-    const int p = A.lists.pair[listed * FEW_T + j];
-    t = p >> 8;
-    return t * R + (p & 255);
-  };
+  const int t = p >> 16, hr = t * R + (p & 0xFFFF);  // the lane's token column: its token, and its row of h and y
   const int wrows = GATE_UP ? 2 * A.Nd : A.Nd;
   const uint32_t row_bytes = (uint32_t)sk_row_bytes(WT, A.Kd);
   typename S::Lanes L;
@@ -286,29 +294,20 @@ __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int listed, i
     L.w_off[f] = c < A.Nd ? r * row_bytes + L.g * 16u : SK_OOB;
     L.s_off[f] = c < A.Nd ? r * s_row + L.g : SK_OOB;
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int j = n * 16 + (lane & 15);
-    L.x_off[n] = SK_OOB;
-    if (j < toks) {
-      int t;
-      const int hr = pair(j, t);
-      L.x_off[n] = (uint32_t)(GATE_UP ? t : hr) * (uint32_t)A.Kd * (uint32_t)sizeof(XT) + L.g * (uint32_t)S::XBYTES;
-    }
-  }
-  sk_f32x4 acc[RT][NT];
-  S::template run<2>(acc, L, wave, (A.Kd + S::STEP - 1) / S::STEP, FEW_W);
-  sk_put<RT, NT>(red, acc);
+  L.x_off[0] = j0 + (lane & 15) < toks ? (uint32_t)(GATE_UP ? t : hr) * (uint32_t)A.Kd * (uint32_t)sizeof(XT) +
+                                             L.g * (uint32_t)S::XBYTES
+                                       : SK_OOB;
+  sk_f32x4 acc[RT][1];
+  S::template run<FEW_D>(acc, L, wave, (A.Kd + S::STEP - 1) / S::STEP, FEW_W);
+  sk_put<RT, 1>(red, acc);
   constexpr int OUT_TILES = GATE_UP ? RT / 2 : RT;
-  for (int i = threadIdx.x; i < OUT_TILES * NT * 64; i += 64 * FEW_W) {
-    const int l = i & 63, n = (i >> 6) % NT, f = (i >> 6) / NT;
-    const int j = n * 16 + (l & 15), c = col0 + f * 16 + 4 * (l >> 4);
-    if (j >= toks || c >= A.Nd) continue;  // Nd % 4 == 0: four columns exist or none
-    int t;
-    const long long o = (long long)pair(j, t) * A.Nd + c;
-    const sk_f32x4 a = sk_get<FEW_W, RT, NT>(red, f, n, l);
+  for (int i = threadIdx.x; i < OUT_TILES * 64; i += 64 * FEW_W) {
+    const int f = i >> 6, c = col0 + f * 16 + 4 * L.g;  // 64 threads to a tile: each its own lane's column
+    if (j0 + (lane & 15) >= toks || c >= A.Nd) continue;  // Nd % 4 == 0: four columns exist or none
+    const long long o = (long long)hr * A.Nd + c;
+    const sk_f32x4 a = sk_get<FEW_W, RT, 1>(red, f, 0, lane);
     if constexpr (GATE_UP) {
-      const sk_f32x4 b = sk_get<FEW_W, RT, NT>(red, f + RT / 2, n, l);
+      const sk_f32x4 b = sk_get<FEW_W, RT, 1>(red, f + RT / 2, 0, lane);
       float v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = silu(a[q]) * b[q];
@@ -328,22 +327,33 @@ __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int listed, i
 
 template <int WT, typename XT, bool GATE_UP>
 __global__ __launch_bounds__(64 * FEW_W) void k_few_product(FewArgs A) {
-  __shared__ sk_f32x4 red[FEW_W * FEW_RT * 2 * 64];
+  __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
   constexpr int COLS = GATE_UP ? FEW_RT * 8 : FEW_RT * 16;  // output columns of an item
   const int tiles = (A.Nd + COLS - 1) / COLS;
   const int e = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * COLS;
+  const int lane = threadIdx.x & 63;
   // the shared experts come first: they have the most tokens
-  int ex = A.Nr + e, listed = -1, toks = A.T;
+  int ex = A.Nr + e, toks = A.T;
+  const int32_t* pairs = nullptr;
+  int p = (lane & 15) << 16 | (A.K + e);
   if (e >= A.Ns) {
-    listed = e - A.Ns;
-    if (listed >= *A.lists.n) return;
-    ex = A.lists.expert[listed];
-    toks = A.lists.tokens[listed];
+    // one memory latency for all four; what lies past the list is not used
+    const int n = *A.lists.n;
+    ex = A.lists.expert[e - A.Ns];
+    toks = A.lists.tokens[e - A.Ns];
+    pairs = A.lists.pair + (e - A.Ns) * FEW_T;
+    p = pairs[lane & 15];
+    if (e - A.Ns >= n) return;
   }
-  if (toks <= 16)
-    few_item<WT, XT, GATE_UP, 1>(A, ex, listed, toks, col0, red);
-  else
-    few_item<WT, XT, GATE_UP, 2>(A, ex, listed, toks, col0, red);
+  // more than 16 tokens: the rows are read again, from a cache that has just
+  // held them
+  for (int j0 = 0; j0 < toks; j0 += 16) {
+    if (j0) {
+      p = pairs ? pairs[j0 + (lane & 15)] : p + (16 << 16);
+      __syncthreads();  // red is read until here
+    }
+    few_item<WT, XT, GATE_UP>(A, ex, toks, j0, p, col0, red);
+  }
 }
 
 // --------------------------------------------------------------- combine --

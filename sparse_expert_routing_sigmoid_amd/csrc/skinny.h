@@ -33,6 +33,7 @@ typedef float sk_f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned sk_u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned sk_u32x2 __attribute__((ext_vector_type(2)));
 
+constexpr int SK_AUX = 0;
 constexpr uint32_t SK_OOB = 0x80000000u;  // past the end of any buffer below 2 GiB
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t sk_rsrc(const void* base, uint32_t bytes) {
@@ -98,7 +99,7 @@ struct Skinny {
       const uint32_t oob = (int)(c + L.g) * EPL < L.K ? 0u : SK_OOB;
 #pragma unroll
       for (int f = 0; f < RT; ++f)
-        st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, 0);
+        st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, SK_AUX);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t xo = L.x_off[n] | oob;
@@ -176,31 +177,38 @@ struct Skinny {
     }
   }
 
-  // Steps s0, s0 + stride, ... below s1, loads D steps ahead.
+  // Steps s0, s0 + stride, ... below s1, loads D steps ahead.  The branches
+  // are uniform: no step past the end is loaded or multiplied (a wave has few
+  // steps, so rounding their number up to D costs more than the branches).
   template <int D>
   __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1, int stride) {
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[f][n] = sk_f32x4{0.f, 0.f, 0.f, 0.f};
-    if (s0 >= s1) return;
-    const int past = (L.K + STEP - 1) / STEP;  // a step that fetches nothing
+    s0 = __builtin_amdgcn_readfirstlane(s0);
     Step st[D];
 #pragma unroll
     for (int i = 0; i < D; ++i) {
-      const int s = s0 + i * stride;
-      load(st[i], L, s < s1 ? s : past);
+      if (s0 + i * stride < s1) load(st[i], L, s0 + i * stride);
       __builtin_amdgcn_sched_barrier(0);
     }
-    for (int s = s0; s < s1; s += D * stride) {
+    int s = s0;
+    for (; s + (2 * D - 1) * stride < s1; s += D * stride) {
 #pragma unroll
       for (int i = 0; i < D; ++i) {
         mma(acc, st[i]);
         __builtin_amdgcn_sched_barrier(0);
-        const int next = s + (D + i) * stride;
-        load(st[i], L, next < s1 ? next : past);
+        load(st[i], L, s + (D + i) * stride);
         __builtin_amdgcn_sched_barrier(0);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * D - 1; ++i) {
+      if (s + i * stride < s1) mma(acc, st[i % D]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < D - 1 && s + (D + i) * stride < s1) load(st[i], L, s + (D + i) * stride);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
