@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64 * LOGIT_W) void k_few_logits(const UT* __restric
   const int s0 = part * steps_per_part;
   const int s1 = s0 + steps_per_part < steps ? s0 + steps_per_part : steps;
   sk_f32x4 acc[1][NT];
-  S::template run<2>(acc, L, s0 + wave, s1, LOGIT_W);
+  S::template run_part<2>(acc, L, s0, s1, wave, LOGIT_W);
   sk_put<1, NT>(red, acc);
   for (int i = threadIdx.x; i < NT * 64; i += 64 * LOGIT_W) {
     const int l = i & 63, n = i >> 6, t = n * 16 + (l & 15);
@@ -264,10 +264,10 @@ struct FewArgs {
 
 // One item: 16 RT weight rows of one expert (gate/up: 8 RT gate rows and the
 // up rows of the same columns of h) on up to 16 of its tokens, j0 and on.
-template <int WT, typename XT, bool GATE_UP>
+template <int WT, typename XT, bool GATE_UP, bool SV>
 __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, int j0, int p, int col0, sk_f32x4* red) {
   constexpr int RT = FEW_RT;
-  using S = Skinny<WT, XT, RT, 1>;
+  using S = Skinny<WT, XT, RT, 1, SV>;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int R = A.K + A.Ns;  // h and y rows of a token
   const int t = p >> 16, hr = t * R + (p & 0xFFFF);  // the lane's token column: its token, and its row of h and y
@@ -292,13 +292,13 @@ __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, int
     const int c = col0 + (GATE_UP ? f % (RT / 2) : f) * 16 + (lane & 15);
     const uint32_t r = (uint32_t)(GATE_UP && f >= RT / 2 ? A.Nd + c : c);
     L.w_off[f] = c < A.Nd ? r * row_bytes + L.g * 16u : SK_OOB;
-    L.s_off[f] = c < A.Nd ? r * s_row + L.g : SK_OOB;
+    L.s_off[f] = c < A.Nd ? r * s_row + (SV ? 0 : L.g) : SK_OOB;
   }
   L.x_off[0] = j0 + (lane & 15) < toks ? (uint32_t)(GATE_UP ? t : hr) * (uint32_t)A.Kd * (uint32_t)sizeof(XT) +
                                              L.g * (uint32_t)S::XBYTES
                                        : SK_OOB;
   sk_f32x4 acc[RT][1];
-  S::template run<FEW_D>(acc, L, wave, (A.Kd + S::STEP - 1) / S::STEP, FEW_W);
+  S::template run_part<SV ? 4 : FEW_D>(acc, L, 0, (A.Kd + S::STEP - 1) / S::STEP, wave, FEW_W);
   sk_put<RT, 1>(red, acc);
   constexpr int OUT_TILES = GATE_UP ? RT / 2 : RT;
   for (int i = threadIdx.x; i < OUT_TILES * 64; i += 64 * FEW_W) {
@@ -325,7 +325,7 @@ __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, int
   }
 }
 
-template <int WT, typename XT, bool GATE_UP>
+template <int WT, typename XT, bool GATE_UP, bool SV>
 __global__ __launch_bounds__(64 * FEW_W) void k_few_product(FewArgs A) {
   __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
   constexpr int COLS = GATE_UP ? FEW_RT * 8 : FEW_RT * 16;  // output columns of an item
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(64 * FEW_W) void k_few_product(FewArgs A) {
       p = pairs ? pairs[j0 + (lane & 15)] : p + (16 << 16);
       __syncthreads();  // red is read until here
     }
-    few_item<WT, XT, GATE_UP>(A, ex, toks, j0, p, col0, red);
+    few_item<WT, XT, GATE_UP, SV>(A, ex, toks, j0, p, col0, red);
   }
 }
 
@@ -379,11 +379,20 @@ __global__ __launch_bounds__(128) void k_few_combine(const RT* resid, const floa
   Vec8<OT>::store(out + (long long)t * d + c, acc);
 }
 
+template <int WT, typename XT, bool GATE_UP>
+void launch_product(FewArgs a, int experts, hipStream_t st) {
+  const int cols = GATE_UP ? FEW_RT * 8 : FEW_RT * 16;
+  const dim3 grid(experts * ((a.Nd + cols - 1) / cols)), block(64 * FEW_W);
+  if (WT == MOE_E2M1 && a.Kd % 128 == 0)
+    hipLaunchKernelGGL((k_few_product<WT, XT, GATE_UP, WT == MOE_E2M1>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_few_product<WT, XT, GATE_UP, false>), grid, block, 0, st, a);
+}
+
 template <int WT, typename XT>
 void launch_products(FewArgs up, FewArgs down, int experts, hipStream_t st) {
-  const int t_up = (up.Nd + FEW_RT * 8 - 1) / (FEW_RT * 8), t_down = (down.Nd + FEW_RT * 16 - 1) / (FEW_RT * 16);
-  hipLaunchKernelGGL((k_few_product<WT, XT, true>), dim3(experts * t_up), dim3(64 * FEW_W), 0, st, up);
-  hipLaunchKernelGGL((k_few_product<WT, XT, false>), dim3(experts * t_down), dim3(64 * FEW_W), 0, st, down);
+  launch_product<WT, XT, true>(up, experts, st);
+  launch_product<WT, XT, false>(down, experts, st);
 }
 
 template <typename UT>

@@ -72,11 +72,11 @@ __global__ __launch_bounds__(256) void k_fp4_dequant(const uint8_t* __restrict__
 // One block: RT 16-row tiles of W and up to 16 NT tokens.
 constexpr int MV_W = 8;  // waves
 
-template <int RT, int NT, typename OT>
+template <int RT, int NT, bool SV, typename OT>
 __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                                                           const uint8_t* __restrict__ scale, int T, long long N, int K,
                                                           OT* __restrict__ y) {
-  using S = Skinny<MOE_E2M1, uint16_t, RT, NT>;
+  using S = Skinny<MOE_E2M1, uint16_t, RT, NT, SV>;
   __shared__ sk_f32x4 red[MV_W * RT * NT * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long long row0 = (long long)blockIdx.x * (16 * RT);
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
   for (int f = 0; f < RT; ++f) {
     const int r = f * 16 + (lane & 15);
     L.w_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 2) + L.g * 16u : SK_OOB;
-    L.s_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 32) + L.g : SK_OOB;
+    L.s_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 32) + (SV ? 0 : L.g) : SK_OOB;
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
     L.x_off[n] = t < toks ? (uint32_t)t * (uint32_t)K * 2u + L.g * (uint32_t)S::XBYTES : SK_OOB;
   }
   sk_f32x4 acc[RT][NT];
-  S::template run<2>(acc, L, wave, (K + S::STEP - 1) / S::STEP, MV_W);
+  S::template run_part<SV ? 4 : 2>(acc, L, 0, (K + S::STEP - 1) / S::STEP, wave, MV_W);
   sk_put<RT, NT>(red, acc);
   for (int e = threadIdx.x; e < RT * NT * 64; e += 64 * MV_W) {
     const int l = e & 63, n = (e >> 6) % NT, f = (e >> 6) / NT;
@@ -181,13 +181,17 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     const dim3 grid((unsigned)ceil_div(N, 16 * rt), (unsigned)ceil_div(T, 16 * nt));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * MV_W), 0, st, static_cast<const uint16_t*>(x), q, scale, T, N, K, out);
   };
-  auto pick = [&](auto* out) {
+  auto shape = [&](auto sv, auto* out) {
+    constexpr bool SV = decltype(sv)::value;
     using OT = std::remove_pointer_t<decltype(out)>;
     if (N >= 16384) {
-      if (T <= 16) go(k_fp4_matvec<4, 1, OT>, 4, 1, out); else go(k_fp4_matvec<4, 2, OT>, 4, 2, out);
+      if (T <= 16) go(k_fp4_matvec<4, 1, SV, OT>, 4, 1, out); else go(k_fp4_matvec<4, 2, SV, OT>, 4, 2, out);
     } else {
-      if (T <= 16) go(k_fp4_matvec<1, 1, OT>, 1, 1, out); else go(k_fp4_matvec<1, 2, OT>, 1, 2, out);
+      if (T <= 16) go(k_fp4_matvec<1, 1, SV, OT>, 1, 1, out); else go(k_fp4_matvec<1, 2, SV, OT>, 1, 2, out);
     }
+  };
+  auto pick = [&](auto* out) {
+    if (K % 128 == 0) shape(std::true_type{}, out); else shape(std::false_type{}, out);
   };
   if (y_t == MOE_BF16) pick(static_cast<uint16_t*>(y)); else pick(static_cast<float*>(y));
   return launch_status("fp4_matvec");

@@ -5,9 +5,8 @@
 // RT row tiles and NT token tiles.  With few tokens the work is reading W
 // once, so the kernel is a stream: weights go from memory to registers with
 // 16-byte loads and never pass through LDS, each step's loads are issued D
-// steps ahead, and the waves of a block share the K axis (wave w takes steps
-// w, w + waves, ...), which keeps a row tile's loads on neighbouring
-// addresses and many bytes in flight; their sums meet in LDS at the end.
+// steps ahead, and the waves of a block share the K axis, which keeps many
+// bytes in flight; their sums meet in LDS at the end.
 //
 // K order.  A step is LD loads of 16 bytes per lane.  Lane l works on weight
 // row l % 16 and on 16-byte chunk c = (step LD + load) 4 + l / 16 of it, i.e.
@@ -68,8 +67,12 @@ __device__ __forceinline__ sk_bf16x8 sk_join(sk_bf16x2 a, sk_bf16x2 b, sk_bf16x2
   return sk_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-template <int WT, typename XT, int RT, int NT>
+// SV: the exponent bytes of E2M1 weights are read 16 at a time, four steps'
+// worth of a row's, which needs rows of a multiple of 4 bytes (K % 128 == 0);
+// otherwise a byte a step.
+template <int WT, typename XT, int RT, int NT, bool SV = false>
 struct Skinny {
+  static_assert(!SV || WT == MOE_E2M1, "only E2M1 has exponent bytes");
   static constexpr int EPL = SkinnyWeight<WT>::EPL, LD = SkinnyWeight<WT>::LD;
   static constexpr int STEP = 4 * EPL * LD;                             // K indices per step
   static constexpr int XBYTES = EPL * (int)sizeof(XT);                  // x bytes of a chunk: 8, 16, 32 or 64
@@ -79,7 +82,7 @@ struct Skinny {
   struct Lanes {
     __amdgpu_buffer_rsrc_t rw, rs, rx;
     uint32_t w_off[RT];  // byte offset of the lane's row of tile f, chunk l / 16 included; SK_OOB: no such row
-    uint32_t s_off[RT];  // E2M1: the same for its exponent bytes
+    uint32_t s_off[RT];  // E2M1: byte offset of its exponent bytes (SV: the row's, else chunk l / 16 included)
     uint32_t x_off[NT];  // byte offset of the lane's token row, chunk l / 16 included; SK_OOB: no such token
     const float* blk_lo;  // E4M3: scales along K of the 128-row block of tiles f < RT / 2, and of the others
     const float* blk_hi;
@@ -91,6 +94,14 @@ struct Skinny {
     uint32_t s[RT];
     float blk[2];
   };
+  struct Scales {
+    sk_u32x4 v[RT];  // word i: the exponent bytes of step i of four
+  };
+
+  __device__ static __forceinline__ void load_scales(Scales& sc, const Lanes& L, int s) {
+#pragma unroll
+    for (int f = 0; f < RT; ++f) sc.v[f] = __builtin_amdgcn_raw_buffer_load_b128(L.rs, L.s_off[f], (uint32_t)s * 4u, 0);
+  }
 
   __device__ static __forceinline__ void load(Step& st, const Lanes& L, int s) {
 #pragma unroll
@@ -112,7 +123,7 @@ struct Skinny {
             st.x[n][l][v] = __builtin_amdgcn_raw_buffer_load_b128(L.rx, xo, c * XBYTES + v * 16u, 0);
         }
       }
-      if (WT == MOE_E2M1) {
+      if (WT == MOE_E2M1 && !SV) {
 #pragma unroll
         for (int f = 0; f < RT; ++f) st.s[f] = __builtin_amdgcn_raw_buffer_load_b8(L.rs, L.s_off[f] | oob, c, 0);
       }
@@ -124,7 +135,8 @@ struct Skinny {
     }
   }
 
-  __device__ static __forceinline__ void mma(sk_f32x4 (&acc)[RT][NT], const Step& st) {
+  __device__ static __forceinline__ void mma(sk_f32x4 (&acc)[RT][NT], const Step& st, const Lanes& L, const Scales& sv,
+                                             int i4) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
       if constexpr (WT == MOE_F32) {
@@ -158,7 +170,8 @@ struct Skinny {
                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(st.w[f][l][2 * j + 1], sc, false),
                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(st.w[f][l][2 * j + 1], sc, true));
           } else {
-            const float sc = __uint_as_float(st.s[f] << 23);  // E8M0: 2^(byte - 127)
+            const uint32_t b = SV ? (sv.v[f][i4] >> (8 * L.g)) & 0xFFu : st.s[f];
+            const float sc = __uint_as_float(b << 23);  // E8M0: 2^(byte - 127)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               a[j] = sk_join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(st.w[f][l][j], sc, 0),
@@ -177,39 +190,53 @@ struct Skinny {
     }
   }
 
-  // Steps s0, s0 + stride, ... below s1, loads D steps ahead.  The branches
-  // are uniform: no step past the end is loaded or multiplied (a wave has few
-  // steps, so rounding their number up to D costs more than the branches).
+  // Steps s0 to s1 - 1, loads D steps ahead.  The branches are uniform: no
+  // step past the end is loaded or multiplied (a wave has few steps, so
+  // rounding their number up to D costs more than the branches).
   template <int D>
-  __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1, int stride) {
+  __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1) {
+    static_assert(!SV || D == 4, "a vector holds the exponent bytes of four steps");
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[f][n] = sk_f32x4{0.f, 0.f, 0.f, 0.f};
     s0 = __builtin_amdgcn_readfirstlane(s0);
+    s1 = __builtin_amdgcn_readfirstlane(s1);
     Step st[D];
+    Scales sc[2];
+    if (SV) load_scales(sc[0], L, s0);
 #pragma unroll
     for (int i = 0; i < D; ++i) {
-      if (s0 + i * stride < s1) load(st[i], L, s0 + i * stride);
+      if (s0 + i < s1) load(st[i], L, s0 + i);
       __builtin_amdgcn_sched_barrier(0);
     }
     int s = s0;
-    for (; s + (2 * D - 1) * stride < s1; s += D * stride) {
+    for (; s + 2 * D - 1 < s1; s += D) {
+      if (SV) load_scales(sc[1], L, s + D);
 #pragma unroll
       for (int i = 0; i < D; ++i) {
-        mma(acc, st[i]);
+        mma(acc, st[i], L, sc[0], i);
         __builtin_amdgcn_sched_barrier(0);
-        load(st[i], L, s + (D + i) * stride);
+        load(st[i], L, s + D + i);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (SV) sc[0] = sc[1];
     }
+    if (SV && s + D < s1) load_scales(sc[1], L, s + D);
 #pragma unroll
     for (int i = 0; i < 2 * D - 1; ++i) {
-      if (s + i * stride < s1) mma(acc, st[i % D]);
+      if (s + i < s1) mma(acc, st[i % D], L, sc[i / D], i % D);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < D - 1 && s + (D + i) * stride < s1) load(st[i], L, s + (D + i) * stride);
+      if (i < D - 1 && s + D + i < s1) load(st[i], L, s + D + i);
       __builtin_amdgcn_sched_barrier(0);
     }
+  }
+
+  // Wave w of W: steps [s0, s1) cut into W runs of equal length (or one less).
+  template <int D>
+  __device__ static __forceinline__ void run_part(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1, int w, int W) {
+    const int n = s1 > s0 ? s1 - s0 : 0;
+    run<D>(acc, L, s0 + n * w / W, s0 + n * (w + 1) / W);
   }
 };
 
