@@ -10,12 +10,31 @@
 // tokens to a matrix instruction; a token that did not select an expert
 // costs nothing there, since an expert's tokens are gathered first.
 //
-//   k_few_logits  partial logits, the K axis split over blocks
-//   k_few_select  one wave per token: scores, selection, gates; then the list
-//                 of touched experts with their tokens
-//   k_few_gate_up h = SiLU(W_gate x) (W_up x) of every (expert, token) pair
-//   k_few_down    y = W_down h of every pair, fp32
-//   k_few_combine the gated sum, in the order residual, shared, routed 0..K-1
+//   k_few_logits  partial logits, the K axis split over blocks; clears the
+//                 counters of the kernels behind it
+//   k_few_select  one block, a wave per token: scores, selection, gates, the
+//                 list of the touched experts and their tokens.  The blocks
+//                 beside it already run the shared experts' gate/up, which
+//                 needs no selection
+//   k_few_up      h = SiLU(W_gate x) (W_up x) of the touched experts, 16
+//                 columns of h of one expert to a block
+//   k_few_down    y = W_down h, fp32, 32 columns of one expert to a block; the
+//                 last block of a column tile forms the gated sum in the order
+//                 residual, shared, routed 0..K-1 (a launch of its own: 72
+//                 against 69 us for the 4-bit layer and one token, 1330
+//                 against 1343 for E4M3 and 32)
+//
+// "Last block": it counts the others' arrivals; nobody waits for anybody
+// inside a kernel.  What such a block reads of the others' results was stored
+// and is loaded at device scope, past the caches of one XCD, and each block
+// counts itself after its stores have completed.
+//
+// Measured against one persistent kernel behind the logits (blocks that take
+// gate/up and then down items from queues, a down item waiting for its
+// expert's gate/up items): 4-bit layer of d = 7168, one token, 75 us against
+// 62; E4M3, 32 tokens, 1433 against 1320.  Its blocks end unevenly (a CU's
+// older waves are served first: 12 us an item against 28 to 49), which the
+// dispatch of fresh blocks evens out.
 #include "skinny.h"
 #include "vec8.h"
 
@@ -28,7 +47,12 @@ constexpr int FEW_W = 4;    // waves of a product block
 constexpr int FEW_RT = 2;   // 16-row tiles of a product block
 constexpr int FEW_D = 2;    // steps a product wave's loads run ahead
 constexpr int LOGIT_W = 8;  // waves of a router block
+constexpr int FEW_THREADS = 64 * FEW_W;
+constexpr int SELECT_W = 8;   // waves of a k_few_select block
 constexpr int LOGIT_PARTS = 8;
+// Words of a cache line: atomics of all XCDs on one line pass at 30 to 40 a
+// microsecond, so busy counters have a line each.
+constexpr int FEW_LINE = 32;
 
 // Touched routed experts, in ascending order, and the tokens of each.
 struct FewLists {
@@ -39,6 +63,8 @@ struct FewLists {
 };
 
 struct FewWs {
+  uint32_t* column_done;  // [ceil(d / 32)] lines: down blocks done of each column tile
+  int n_column_done;      // words
   float* z;  // [parts, T, Nr]
   FewLists lists;
   void* h;   // [T (K + Ns), I], row t (K + Ns) + k; shared expert j is k = K + j
@@ -67,6 +93,9 @@ FewWs few_ws(void* base, int T, int d, int Nr, int Ns, int I, int K, moe_dtype u
     return p;
   };
   const size_t pairs = (size_t)T * (K + Ns);
+  const int columns = (d + FEW_RT * 16 - 1) / (FEW_RT * 16);
+  w.n_column_done = columns * FEW_LINE;
+  w.column_done = reinterpret_cast<uint32_t*>(take((size_t)w.n_column_done * 4));
   w.z = reinterpret_cast<float*>(take((size_t)few_parts(d, Nr) * T * Nr * 4));
   w.lists.n = reinterpret_cast<int32_t*>(take(4));
   w.lists.expert = reinterpret_cast<int32_t*>(take((size_t)Nr * 4));
@@ -82,7 +111,11 @@ FewWs few_ws(void* base, int T, int d, int Nr, int Ns, int I, int K, moe_dtype u
 template <typename UT, int NT>
 __global__ __launch_bounds__(64 * LOGIT_W) void k_few_logits(const UT* __restrict__ u, const float* __restrict__ e,
                                                              int T, int d, int Nr, int steps_per_part,
-                                                             float* __restrict__ z) {
+                                                             float* __restrict__ z, uint32_t* __restrict__ ctl,
+                                                             int n_ctl) {
+  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * 64 * LOGIT_W + threadIdx.x; i < n_ctl;
+       i += gridDim.x * gridDim.y * 64 * LOGIT_W)
+    ctl[i] = 0;
   using S = Skinny<MOE_F32, UT, 1, NT>;
   __shared__ sk_f32x4 red[LOGIT_W * NT * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -104,7 +137,7 @@ __global__ __launch_bounds__(64 * LOGIT_W) void k_few_logits(const UT* __restric
   const int s1 = s0 + steps_per_part < steps ? s0 + steps_per_part : steps;
   sk_f32x4 acc[1][NT];
   S::template run_part<2>(acc, L, s0, s1, wave, LOGIT_W);
-  sk_put<1, NT>(red, acc);
+  sk_put<1, NT>(red, acc, threadIdx.x);
   for (int i = threadIdx.x; i < NT * 64; i += 64 * LOGIT_W) {
     const int l = i & 63, n = i >> 6, t = n * 16 + (l & 15);
     if (t >= T) continue;
@@ -115,6 +148,24 @@ __global__ __launch_bounds__(64 * LOGIT_W) void k_few_logits(const UT* __restric
       if (ex < Nr) z[((long long)part * T + t) * Nr + ex] = s[j];
     }
   }
+}
+
+template <typename V>
+__device__ __forceinline__ void few_post(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void few_post4(float* p, sk_f32x4 v) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  few_post(q, (uint64_t)__float_as_uint(v[1]) << 32 | __float_as_uint(v[0]));
+  few_post(q + 1, (uint64_t)__float_as_uint(v[3]) << 32 | __float_as_uint(v[2]));
+}
+__device__ __forceinline__ sk_f32x4 few_peek4(const float* p) {
+  const uint64_t* q = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t a = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return sk_f32x4{__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32)), __uint_as_float((uint32_t)b),
+                  __uint_as_float((uint32_t)(b >> 32))};
 }
 
 // Largest v of the wave (row shifts, then the rows' last lanes are passed on;
@@ -135,10 +186,10 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 // tie to the lowest index.  An expert's bit in `mask` gains the token.
 template <int EPL>
 __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int parts, const float* __restrict__ bias,
-                                                int t, int T, int Nr, int K, int32_t* __restrict__ topk_idx,
-                                                float* __restrict__ topk_gate, float* __restrict__ topk_score,
+                                                int t, int lane, int T, int Nr, int K,
+                                                int32_t* topk_idx,
+                                                float* topk_gate, float* topk_score, uint16_t* pick,
                                                 uint32_t* mask) {
-  const int lane = threadIdx.x & 63;
   float s[EPL];
   uint32_t key[EPL];
   uint32_t avail = 0;
@@ -201,50 +252,11 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
   if (lane < K) {
     const int o = t * K + lane;
     topk_idx[o] = my_idx;
+    pick[o] = (uint16_t)my_idx;
     topk_gate[o] = my_s / sum;
     if (topk_score) topk_score[o] = my_s;
     atomicOr(&mask[my_idx], 1u << t);
   }
-}
-
-template <int EPL>
-__global__ __launch_bounds__(1024) void k_few_select(const float* __restrict__ z, int parts,
-                                                     const float* __restrict__ bias, int T, int Nr, int K,
-                                                     int32_t* __restrict__ topk_idx, float* __restrict__ topk_gate,
-                                                     float* __restrict__ topk_score, int32_t* __restrict__ load,
-                                                     FewLists lists) {
-  __shared__ uint32_t mask[MOE_MAX_EXPERTS];  // tokens of each expert
-  __shared__ int place[MOE_MAX_EXPERTS];      // its position in the list
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < Nr; i += 1024) mask[i] = 0;
-  __syncthreads();
-  for (int t = wave; t < T; t += 16)
-    few_route_token<EPL>(z, parts, bias, t, T, Nr, K, topk_idx, topk_gate, topk_score, mask);
-  __threadfence_block();  // topk_idx is read back below
-  __syncthreads();
-  if (wave == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < Nr; i0 += 64) {
-      const int i = i0 + lane;
-      const bool touched = i < Nr && mask[i] != 0;
-      const unsigned long long b = __ballot(touched);
-      const int at = n + __popcll(b & ((1ull << lane) - 1));
-      if (touched) {
-        place[i] = at;
-        lists.expert[at] = i;
-        lists.tokens[at] = __popc(mask[i]);
-      }
-      n += __popcll(b);
-    }
-    if (lane == 0) *lists.n = n;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < T * K; i += 1024) {
-    const int t = i / K, k = i % K, ex = topk_idx[i];
-    lists.pair[place[ex] * FEW_T + __popc(mask[ex] & ((1u << t) - 1))] = t << 16 | k;
-  }
-  if (load)
-    for (int i = threadIdx.x; i < Nr; i += 1024) load[i] = __popc(mask[i]);
 }
 
 __global__ void k_few_no_load(int32_t* load, int Nr) {
@@ -252,167 +264,295 @@ __global__ void k_few_no_load(int32_t* load, int Nr) {
   if (i < Nr) load[i] = 0;
 }
 
-// -------------------------------------------------------------- products --
+// -------------------------------------------------- selection, products --
 struct FewArgs {
-  const void* x;      // gate/up: tokens u [T, Kd]; down: h [T (K + Ns), Kd]
-  const void* w;      // [Nr + Ns, rows, Kd] as stored
-  const void* scale;  // E4M3: fp32 [E, rows / 128, Kd / 128]; E2M1: bytes [E, rows, Kd / 32]
-  void* out;          // gate/up: h [T (K + Ns), Nd]; down: y [T (K + Ns), Nd] fp32
+  const void* u;  // [T, d]
+  const void* w13;
+  const void* w13_scale;
+  const void* w2;
+  const void* w2_scale;
+  const float* z;
+  const float* bias;
+  const void* resid;  // [T, d] or NULL
+  int32_t* topk_idx;
+  float* topk_gate;
+  float* topk_score;
+  int32_t* load;
+  void* h;
+  float* y;
+  void* out;  // [T, d]
+  uint32_t* column_done;
   FewLists lists;
-  int T, K, Nr, Ns, Nd, Kd;
+  int T, d, Nr, Ns, I, K, parts;
+  bool resid_bf16, out_bf16;
 };
+
+// The block's device-scope stores have completed, and the counter has counted
+// them.  Returns the counter's value before, to every thread.
+__device__ __forceinline__ uint32_t few_signal(uint32_t* counter, uint32_t* shared, int tid) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0)
+    *shared = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return *shared;
+}
+
+struct FewSelect {
+  uint32_t mask[MOE_MAX_EXPERTS];     // tokens of each expert
+  uint16_t place[MOE_MAX_EXPERTS];    // its place in the list
+  uint16_t pick[FEW_T * MOE_MAX_K];   // [T, K] selected experts
+};
+
+__device__ __forceinline__ void few_select(const FewArgs& A, FewSelect& S, int tid) {
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int e = tid; e < A.Nr; e += 64 * SELECT_W) S.mask[e] = 0;
+  __syncthreads();
+  for (int t = wave; t < A.T; t += SELECT_W) {
+    if (A.Nr <= 64)
+      few_route_token<1>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
+                         S.mask);
+    else if (A.Nr <= 256)
+      few_route_token<4>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
+                         S.mask);
+    else
+      few_route_token<16>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
+                          S.mask);
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int n = 0;
+    for (int e0 = 0; e0 < A.Nr; e0 += 64) {
+      const int e = e0 + lane;
+      const uint32_t m = e < A.Nr ? S.mask[e] : 0u;
+      const unsigned long long b = __ballot(m != 0);
+      const int at = n + __popcll(b & ((1ull << lane) - 1));
+      if (m) {
+        S.place[e] = (uint16_t)at;
+        A.lists.expert[at] = e;
+        A.lists.tokens[at] = __popc(m);
+      }
+      n += __popcll(b);
+    }
+    if (lane == 0) *A.lists.n = n;
+  }
+  if (A.load)
+    for (int e = tid; e < A.Nr; e += 64 * SELECT_W) A.load[e] = __popc(S.mask[e]);
+  __syncthreads();
+  for (int q = tid; q < A.T * A.K; q += 64 * SELECT_W) {
+    const int t = q / A.K, e = S.pick[q];
+    A.lists.pair[S.place[e] * FEW_T + __popc(S.mask[e] & ((1u << t) - 1))] = t << 16 | (q - t * A.K);
+  }
+}
 
 // One item: 16 RT weight rows of one expert (gate/up: 8 RT gate rows and the
 // up rows of the same columns of h) on up to 16 of its tokens, j0 and on.
-template <int WT, typename XT, bool GATE_UP, bool SV>
-__device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, int j0, int p, int col0, sk_f32x4* red) {
+// p: token and slot of the lane's token column.
+template <int WT, typename XT, bool UP, bool SV, int W>
+__device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, int j0, int p, int col0,
+                                            sk_f32x4* red, int tid) {
   constexpr int RT = FEW_RT;
   using S = Skinny<WT, XT, RT, 1, SV>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int Kd = UP ? A.d : A.I, Nd = UP ? A.I : A.d;
+  const int lane = tid & 63, wave = tid >> 6;
   const int R = A.K + A.Ns;  // h and y rows of a token
-  const int t = p >> 16, hr = t * R + (p & 0xFFFF);  // the lane's token column: its token, and its row of h and y
-  const int wrows = GATE_UP ? 2 * A.Nd : A.Nd;
-  const uint32_t row_bytes = (uint32_t)sk_row_bytes(WT, A.Kd);
+  const int t = p >> 16, hr = t * R + (p & 0xFFFF);
+  const int wrows = UP ? 2 * Nd : Nd;
+  const uint32_t row_bytes = (uint32_t)sk_row_bytes(WT, Kd);
+  const void* scale = UP ? A.w13_scale : A.w2_scale;
   typename S::Lanes L;
-  L.K = A.Kd;
+  L.K = Kd;
   L.g = lane >> 4;
-  L.rw = sk_rsrc(static_cast<const uint8_t*>(A.w) + (long long)ex * wrows * row_bytes, (uint32_t)wrows * row_bytes);
-  L.rx = sk_rsrc(A.x, (uint32_t)(GATE_UP ? A.T : A.T * R) * (uint32_t)A.Kd * (uint32_t)sizeof(XT));
-  const uint32_t s_row = (uint32_t)A.Kd / 32u;
+  L.rw = sk_rsrc(static_cast<const uint8_t*>(UP ? A.w13 : A.w2) + (long long)ex * wrows * row_bytes,
+                 (uint32_t)wrows * row_bytes);
+  L.rx = sk_rsrc(UP ? A.u : A.h, (uint32_t)(UP ? A.T : A.T * R) * (uint32_t)Kd * (uint32_t)sizeof(XT));
+  const uint32_t s_row = (uint32_t)Kd / 32u;
   if (WT == MOE_E2M1)
-    L.rs = sk_rsrc(static_cast<const uint8_t*>(A.scale) + (long long)ex * wrows * s_row, (uint32_t)wrows * s_row);
+    L.rs = sk_rsrc(static_cast<const uint8_t*>(scale) + (long long)ex * wrows * s_row, (uint32_t)wrows * s_row);
   if (WT == MOE_E4M3) {
-    const int nk = A.Kd / 128;
-    const float* sc = static_cast<const float*>(A.scale) + (long long)ex * (wrows / 128) * nk;
+    const int nk = Kd / 128;
+    const float* sc = static_cast<const float*>(scale) + (long long)ex * (wrows / 128) * nk;
     L.blk_lo = sc + (long long)(col0 / 128) * nk;
-    L.blk_hi = sc + (long long)((GATE_UP ? A.Nd + col0 : col0) / 128) * nk;
+    L.blk_hi = sc + (long long)((UP ? Nd + col0 : col0) / 128) * nk;
   }
 #pragma unroll
   for (int f = 0; f < RT; ++f) {
-    const int c = col0 + (GATE_UP ? f % (RT / 2) : f) * 16 + (lane & 15);
-    const uint32_t r = (uint32_t)(GATE_UP && f >= RT / 2 ? A.Nd + c : c);
-    L.w_off[f] = c < A.Nd ? r * row_bytes + L.g * 16u : SK_OOB;
-    L.s_off[f] = c < A.Nd ? r * s_row + (SV ? 0 : L.g) : SK_OOB;
+    const int c = col0 + (UP ? f % (RT / 2) : f) * 16 + (lane & 15);
+    const uint32_t r = (uint32_t)(UP && f >= RT / 2 ? Nd + c : c);
+    L.w_off[f] = c < Nd ? r * row_bytes + L.g * 16u : SK_OOB;
+    L.s_off[f] = c < Nd ? r * s_row + (SV ? 0 : L.g) : SK_OOB;
   }
-  L.x_off[0] = j0 + (lane & 15) < toks ? (uint32_t)(GATE_UP ? t : hr) * (uint32_t)A.Kd * (uint32_t)sizeof(XT) +
+  L.x_off[0] = j0 + (lane & 15) < toks ? (uint32_t)(UP ? t : hr) * (uint32_t)Kd * (uint32_t)sizeof(XT) +
                                              L.g * (uint32_t)S::XBYTES
                                        : SK_OOB;
   sk_f32x4 acc[RT][1];
-  S::template run_part<SV ? 4 : FEW_D>(acc, L, 0, (A.Kd + S::STEP - 1) / S::STEP, wave, FEW_W);
-  sk_put<RT, 1>(red, acc);
-  constexpr int OUT_TILES = GATE_UP ? RT / 2 : RT;
-  for (int i = threadIdx.x; i < OUT_TILES * 64; i += 64 * FEW_W) {
+  S::template run_part<FEW_D>(acc, L, 0, (Kd + S::STEP - 1) / S::STEP, wave, W);
+  sk_put<RT, 1>(red, acc, tid);
+  constexpr int OUT_TILES = UP ? RT / 2 : RT;
+  for (int i = tid; i < OUT_TILES * 64; i += 64 * W) {
     const int f = i >> 6, c = col0 + f * 16 + 4 * L.g;  // 64 threads to a tile: each its own lane's column
-    if (j0 + (lane & 15) >= toks || c >= A.Nd) continue;  // Nd % 4 == 0: four columns exist or none
-    const long long o = (long long)hr * A.Nd + c;
-    const sk_f32x4 a = sk_get<FEW_W, RT, 1>(red, f, 0, lane);
-    if constexpr (GATE_UP) {
-      const sk_f32x4 b = sk_get<FEW_W, RT, 1>(red, f + RT / 2, 0, lane);
+    if (j0 + (lane & 15) >= toks || c >= Nd) continue;  // Nd % 4 == 0: four columns exist or none
+    const long long o = (long long)hr * Nd + c;
+    const sk_f32x4 a = sk_get<W, RT, 1>(red, f, 0, lane);
+    if constexpr (UP) {
+      const sk_f32x4 b = sk_get<W, RT, 1>(red, f + RT / 2, 0, lane);
       float v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = silu(a[q]) * b[q];
       if constexpr (sizeof(XT) == 4) {
-        *reinterpret_cast<sk_f32x4*>(static_cast<float*>(A.out) + o) = sk_f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<sk_f32x4*>(static_cast<float*>(A.h) + o) = sk_f32x4{v[0], v[1], v[2], v[3]};
       } else {
         // h is rounded to bf16, as the operand of the down projection's
         // matrix instructions (fp32 layers keep it in fp32)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + o) =
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.h) + o) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
     } else {
-      *reinterpret_cast<sk_f32x4*>(static_cast<float*>(A.out) + o) = a;
+      few_post4(A.y + o, a);
     }
   }
 }
 
-template <int WT, typename XT, bool GATE_UP, bool SV>
-__global__ __launch_bounds__(64 * FEW_W) void k_few_product(FewArgs A) {
+__device__ __forceinline__ sk_f32x4 few_load4(const void* p, bool bf16, long long i) {
+  if (!bf16) return *reinterpret_cast<const sk_f32x4*>(static_cast<const float*>(p) + i);
+  const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  return sk_f32x4{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u), __uint_as_float(q.y << 16),
+                  __uint_as_float(q.y & 0xFFFF0000u)};
+}
+
+// out[:, col0 .. col0 + 31], eight threads to a token.
+__device__ __forceinline__ void few_combine(const FewArgs& A, int col0, int tid) {
+  constexpr int PER = FEW_RT * 4;  // threads to a token, four columns each
+  const int t = tid / PER, c = col0 + (tid % PER) * 4;
+  if (c >= A.d) return;
+  for (int tt = t; tt < A.T; tt += FEW_THREADS / PER) {
+    const long long o = (long long)tt * A.d + c;
+    const float* y = A.y + (long long)tt * (A.K + A.Ns) * A.d + c;
+    sk_f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (A.resid) s = few_load4(A.resid, A.resid_bf16, o);
+    for (int j = 0; j < A.Ns; ++j) s += few_peek4(y + (long long)(A.K + j) * A.d);
+    for (int k0 = 0; k0 < A.K; k0 += 4) {
+      sk_f32x4 v[4];
+      float g[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int kk = k0 + k < A.K ? k0 + k : k0;
+        v[k] = few_peek4(y + (long long)kk * A.d);
+        g[k] = A.topk_gate[tt * A.K + kk];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < A.K)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) s[q] = fmaf(g[k], v[k][q], s[q]);
+    }
+    if (A.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + o) =
+          make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    else
+      *reinterpret_cast<sk_f32x4*>(static_cast<float*>(A.out) + o) = s;
+  }
+}
+
+// An expert's column tile on all its tokens.  More than 16: the rows are read
+// again, from a cache that has just held them.
+template <int WT, typename XT, bool UP, bool SV, int W>
+__device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, const int32_t* pairs, int p, int col0,
+                                         sk_f32x4* red, int tid) {
+  for (int j0 = 0; j0 < toks; j0 += 16) {
+    if (j0) {
+      p = pairs ? pairs[j0 + (tid & 15)] : p + (16 << 16);
+      __syncthreads();  // red is read until here
+    }
+    few_product<WT, XT, UP, SV, W>(A, ex, toks, j0, p, col0, red, tid);
+  }
+}
+
+constexpr int FEW_UP_COLS = FEW_RT * 8, FEW_DOWN_COLS = FEW_RT * 16;  // columns of a block
+
+// Block 0 selects; the others are the shared experts' gate/up, with many
+// waves to a block: they are alone on the chip.
+template <int WT, typename XT, bool SV>
+__global__ __launch_bounds__(64 * SELECT_W) void k_few_select(FewArgs A) {
+  __shared__ union {
+    sk_f32x4 red[SELECT_W * FEW_RT * 64];
+    FewSelect select;
+  } lds;
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    few_select(A, lds.select, tid);
+    return;
+  }
+  const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS;
+  const int item = blockIdx.x - 1, e = item / tiles;
+  few_item<WT, XT, true, SV, SELECT_W>(A, A.Nr + e, A.T, nullptr, (tid & 15) << 16 | (A.K + e), (item % tiles) * FEW_UP_COLS,
+                             lds.red, tid);
+}
+
+template <int WT, typename XT, bool SV>
+__global__ __launch_bounds__(FEW_THREADS) void k_few_up(FewArgs A) {
   __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
-  constexpr int COLS = GATE_UP ? FEW_RT * 8 : FEW_RT * 16;  // output columns of an item
-  const int tiles = (A.Nd + COLS - 1) / COLS;
-  const int e = blockIdx.x / tiles, col0 = (blockIdx.x % tiles) * COLS;
-  const int lane = threadIdx.x & 63;
-  // the shared experts come first: they have the most tokens
-  int ex = A.Nr + e, toks = A.T;
+  const int tid = threadIdx.x;
+  const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, e = blockIdx.x / tiles;
+  // one memory latency for all four; what lies past the list is not used
+  const int n = *A.lists.n, ex = A.lists.expert[e], toks = A.lists.tokens[e];
+  const int32_t* pairs = A.lists.pair + e * FEW_T;
+  const int p = pairs[tid & 15];
+  if (e >= n) return;
+  few_item<WT, XT, true, SV, FEW_W>(A, ex, toks, pairs, p, (blockIdx.x % tiles) * FEW_UP_COLS, red, tid);
+}
+
+template <int WT, typename XT, bool SV>
+__global__ __launch_bounds__(FEW_THREADS) void k_few_down(FewArgs A) {
+  __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
+  __shared__ uint32_t s_count;
+  const int tid = threadIdx.x;
+  const int tiles = (A.d + FEW_DOWN_COLS - 1) / FEW_DOWN_COLS, e = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+  const int n = *A.lists.n;
+  int ex = A.Nr + e, toks = A.T, p = (tid & 15) << 16 | (A.K + e);
   const int32_t* pairs = nullptr;
-  int p = (lane & 15) << 16 | (A.K + e);
-  if (e >= A.Ns) {
-    // one memory latency for all four; what lies past the list is not used
-    const int n = *A.lists.n;
+  if (e >= A.Ns) {  // the shared experts come first: they have the most tokens
     ex = A.lists.expert[e - A.Ns];
     toks = A.lists.tokens[e - A.Ns];
     pairs = A.lists.pair + (e - A.Ns) * FEW_T;
-    p = pairs[lane & 15];
+    p = pairs[tid & 15];
     if (e - A.Ns >= n) return;
   }
-  // more than 16 tokens: the rows are read again, from a cache that has just
-  // held them
-  for (int j0 = 0; j0 < toks; j0 += 16) {
-    if (j0) {
-      p = pairs ? pairs[j0 + (lane & 15)] : p + (16 << 16);
-      __syncthreads();  // red is read until here
-    }
-    few_item<WT, XT, GATE_UP, SV>(A, ex, toks, j0, p, col0, red);
-  }
+  few_item<WT, XT, false, SV, FEW_W>(A, ex, toks, pairs, p, tile * FEW_DOWN_COLS, red, tid);
+  if (few_signal(A.column_done + tile * FEW_LINE, &s_count, tid) == (uint32_t)(A.Ns + n) - 1)
+    few_combine(A, tile * FEW_DOWN_COLS, tid);
 }
 
-// --------------------------------------------------------------- combine --
-template <typename RT, typename OT>
-__global__ __launch_bounds__(128) void k_few_combine(const RT* resid, const float* __restrict__ y,
-                                                     const float* __restrict__ gate, int d, int K, int Ns, OT* out) {
-  const int t = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 8;
-  if (c >= d) return;
-  float acc[8] = {}, v[8];
-  if (resid) Vec8<RT>::load(resid + (long long)t * d + c, acc);
-  const float* yt = y + (long long)t * (K + Ns) * d + c;
-  for (int j = 0; j < Ns; ++j) {
-    Vec8<float>::load(yt + (long long)(K + j) * d, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += v[i];
-  }
-  for (int k = 0; k < K; ++k) {
-    const float g = gate[t * K + k];
-    Vec8<float>::load(yt + (long long)k * d, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[i], acc[i]);
-  }
-  Vec8<OT>::store(out + (long long)t * d + c, acc);
-}
-
-template <int WT, typename XT, bool GATE_UP>
-void launch_product(FewArgs a, int experts, hipStream_t st) {
-  const int cols = GATE_UP ? FEW_RT * 8 : FEW_RT * 16;
-  const dim3 grid(experts * ((a.Nd + cols - 1) / cols)), block(64 * FEW_W);
-  if (WT == MOE_E2M1 && a.Kd % 128 == 0)
-    hipLaunchKernelGGL((k_few_product<WT, XT, GATE_UP, WT == MOE_E2M1>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_few_product<WT, XT, GATE_UP, false>), grid, block, 0, st, a);
+template <int WT, typename XT, bool SV>
+void launch_blocks(const FewArgs& A, hipStream_t st) {
+  const int touched = A.T * A.K < A.Nr ? A.T * A.K : A.Nr;
+  const int up = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, down = (A.d + FEW_DOWN_COLS - 1) / FEW_DOWN_COLS;
+  const dim3 block(FEW_THREADS);
+  hipLaunchKernelGGL((k_few_select<WT, XT, SV>), dim3(1 + A.Ns * up), dim3(64 * SELECT_W), 0, st, A);
+  hipLaunchKernelGGL((k_few_up<WT, XT, SV>), dim3(touched * up), block, 0, st, A);
+  hipLaunchKernelGGL((k_few_down<WT, XT, SV>), dim3((touched + A.Ns) * down), block, 0, st, A);
 }
 
 template <int WT, typename XT>
-void launch_products(FewArgs up, FewArgs down, int experts, hipStream_t st) {
-  launch_product<WT, XT, true>(up, experts, st);
-  launch_product<WT, XT, false>(down, experts, st);
+void launch_layer(const FewArgs& A, hipStream_t st) {
+  if (WT == MOE_E2M1 && A.d % 128 == 0 && A.I % 128 == 0)
+    launch_blocks<WT, XT, WT == MOE_E2M1>(A, st);
+  else
+    launch_blocks<WT, XT, false>(A, st);
 }
 
 template <typename UT>
-void launch_logits(const void* u, const float* e, int T, int d, int Nr, int parts, float* z, hipStream_t st) {
+void launch_logits(const void* u, const float* e, int T, int d, int Nr, int parts, float* z, uint32_t* ctl, int n_ctl,
+                   hipStream_t st) {
   const int step = Skinny<MOE_F32, UT, 1, 1>::STEP, steps = (d + step - 1) / step;
   const int per = (steps + parts - 1) / parts;
   const dim3 grid((Nr + 15) / 16, parts);
   if (T <= 16)
     hipLaunchKernelGGL((k_few_logits<UT, 1>), grid, dim3(64 * LOGIT_W), 0, st, static_cast<const UT*>(u), e, T, d, Nr,
-                       per, z);
+                       per, z, ctl, n_ctl);
   else
     hipLaunchKernelGGL((k_few_logits<UT, 2>), grid, dim3(64 * LOGIT_W), 0, st, static_cast<const UT*>(u), e, T, d, Nr,
-                       per, z);
-}
-
-template <typename RT, typename OT>
-void launch_combine(const void* resid, const float* y, const float* gate, int T, int d, int K, int Ns, void* out,
-                    hipStream_t st) {
-  hipLaunchKernelGGL((k_few_combine<RT, OT>), dim3(T, (unsigned)ceil_div(d, 1024)), dim3(128), 0, st,
-                     static_cast<const RT*>(resid), y, gate, d, K, Ns, static_cast<OT*>(out));
+                       per, z, ctl, n_ctl);
 }
 
 bool few_sizes_ok(int T, int d, int Nr, int Ns, int I, int K) {
@@ -468,35 +608,17 @@ moe_status layer_few(const void* u, moe_dtype u_t, const float* centroids, const
   const FewWs w = few_ws(ws, T, d, Nr, Ns, I, K, u_t);
   const int parts = few_parts(d, Nr);
   if (u_t == MOE_F32)
-    launch_logits<float>(u, centroids, T, d, Nr, parts, w.z, st);
+    launch_logits<float>(u, centroids, T, d, Nr, parts, w.z, w.column_done, w.n_column_done, st);
   else
-    launch_logits<uint16_t>(u, centroids, T, d, Nr, parts, w.z, st);
-  auto select = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, st, w.z, parts, bias, T, Nr, K, topk_idx, topk_gate, topk_score,
-                       expert_load, w.lists);
-  };
-  if (Nr <= 64)
-    select(k_few_select<1>);
-  else if (Nr <= 256)
-    select(k_few_select<4>);
-  else
-    select(k_few_select<16>);
-  const FewArgs up{u, w13, w13_scale, w.h, w.lists, T, K, Nr, Ns, I, d};
-  const FewArgs down{w.h, w2, w2_scale, w.y, w.lists, T, K, Nr, Ns, d, I};
-  const int experts = Ns + (T * K < Nr ? T * K : Nr);
+    launch_logits<uint16_t>(u, centroids, T, d, Nr, parts, w.z, w.column_done, w.n_column_done, st);
+  const FewArgs A{u,          w13,        w13_scale,   w2,  w2_scale, w.z, bias,  resid,   topk_idx, topk_gate,
+                  topk_score, expert_load, w.h,        w.y, out,      w.column_done, w.lists, T, d, Nr,
+                  Ns,         I,          K,           parts, r_t == MOE_BF16, out_t == MOE_BF16};
   switch (w_t) {
-    case MOE_F32: launch_products<MOE_F32, float>(up, down, experts, st); break;
-    case MOE_BF16: launch_products<MOE_BF16, uint16_t>(up, down, experts, st); break;
-    case MOE_E4M3: launch_products<MOE_E4M3, uint16_t>(up, down, experts, st); break;
-    default: launch_products<MOE_E2M1, uint16_t>(up, down, experts, st); break;
-  }
-  const bool rf = !resid || r_t == MOE_F32;
-  if (out_t == MOE_F32) {
-    if (rf) launch_combine<float, float>(resid, w.y, topk_gate, T, d, K, Ns, out, st);
-    else launch_combine<uint16_t, float>(resid, w.y, topk_gate, T, d, K, Ns, out, st);
-  } else {
-    if (rf) launch_combine<float, uint16_t>(resid, w.y, topk_gate, T, d, K, Ns, out, st);
-    else launch_combine<uint16_t, uint16_t>(resid, w.y, topk_gate, T, d, K, Ns, out, st);
+    case MOE_F32: launch_layer<MOE_F32, float>(A, st); break;
+    case MOE_BF16: launch_layer<MOE_BF16, uint16_t>(A, st); break;
+    case MOE_E4M3: launch_layer<MOE_E4M3, uint16_t>(A, st); break;
+    default: launch_layer<MOE_E2M1, uint16_t>(A, st); break;
   }
   return launch_status("moe_layer_few");
 }

@@ -101,8 +101,8 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
     L.x_off[n] = t < toks ? (uint32_t)t * (uint32_t)K * 2u + L.g * (uint32_t)S::XBYTES : SK_OOB;
   }
   sk_f32x4 acc[RT][NT];
-  S::template run_part<SV ? 4 : 2>(acc, L, 0, (K + S::STEP - 1) / S::STEP, wave, MV_W);
-  sk_put<RT, NT>(red, acc);
+  S::template run_part<2>(acc, L, 0, (K + S::STEP - 1) / S::STEP, wave, MV_W);
+  sk_put<RT, NT>(red, acc, threadIdx.x);
   for (int e = threadIdx.x; e < RT * NT * 64; e += 64 * MV_W) {
     const int l = e & 63, n = (e >> 6) % NT, f = (e >> 6) / NT;
     const int t = n * 16 + (l & 15), r = f * 16 + 4 * (l >> 4);

@@ -32,7 +32,6 @@ typedef float sk_f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned sk_u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned sk_u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int SK_AUX = 0;
 constexpr uint32_t SK_OOB = 0x80000000u;  // past the end of any buffer below 2 GiB
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t sk_rsrc(const void* base, uint32_t bytes) {
@@ -110,7 +109,7 @@ struct Skinny {
       const uint32_t oob = (int)(c + L.g) * EPL < L.K ? 0u : SK_OOB;
 #pragma unroll
       for (int f = 0; f < RT; ++f)
-        st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, SK_AUX);
+        st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, 0);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t xo = L.x_off[n] | oob;
@@ -195,7 +194,8 @@ struct Skinny {
   // rounding their number up to D costs more than the branches).
   template <int D>
   __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1) {
-    static_assert(!SV || D == 4, "a vector holds the exponent bytes of four steps");
+    constexpr int U = SV ? 4 : D;  // steps to a turn of the loop: a vector holds the exponent bytes of four
+    static_assert(U % D == 0, "a turn of the loop goes round the ring");
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
@@ -211,23 +211,23 @@ struct Skinny {
       __builtin_amdgcn_sched_barrier(0);
     }
     int s = s0;
-    for (; s + 2 * D - 1 < s1; s += D) {
-      if (SV) load_scales(sc[1], L, s + D);
+    for (; s + U + D - 1 < s1; s += U) {
+      if (SV) load_scales(sc[1], L, s + U);
 #pragma unroll
-      for (int i = 0; i < D; ++i) {
-        mma(acc, st[i], L, sc[0], i);
+      for (int i = 0; i < U; ++i) {
+        mma(acc, st[i % D], L, sc[0], i);
         __builtin_amdgcn_sched_barrier(0);
-        load(st[i], L, s + D + i);
+        load(st[i % D], L, s + D + i);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (SV) sc[0] = sc[1];
     }
-    if (SV && s + D < s1) load_scales(sc[1], L, s + D);
+    if (SV && s + U < s1) load_scales(sc[1], L, s + U);
 #pragma unroll
-    for (int i = 0; i < 2 * D - 1; ++i) {
-      if (s + i < s1) mma(acc, st[i % D], L, sc[i / D], i % D);
+    for (int i = 0; i < U + D - 1; ++i) {
+      if (s + i < s1) mma(acc, st[i % D], L, sc[i / U], i % U);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < D - 1 && s + D + i < s1) load(st[i], L, s + D + i);
+      if (i < U - 1 && s + D + i < s1) load(st[i % D], L, s + D + i);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -244,8 +244,8 @@ struct Skinny {
 // Element (f, n, lane) of the sum: rows 4 (lane / 16) + 0..3 of tile f, token
 // lane % 16 of tile n.
 template <int RT, int NT>
-__device__ __forceinline__ void sk_put(sk_f32x4* red, const sk_f32x4 (&acc)[RT][NT]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__device__ __forceinline__ void sk_put(sk_f32x4* red, const sk_f32x4 (&acc)[RT][NT], int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int f = 0; f < RT; ++f)
 #pragma unroll
