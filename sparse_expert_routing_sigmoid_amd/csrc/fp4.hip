@@ -69,6 +69,18 @@ __global__ __launch_bounds__(256) void k_fp4_dequant(const uint8_t* __restrict__
   Vec8<OT>::store(out + i * 8, v);
 }
 
+template <typename OT>
+__device__ __forceinline__ void mv_store(OT* o, const sk_f32x4& s, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) {
+      if constexpr (sizeof(OT) == 2)
+        o[i] = f32_to_bf16(s[i]);
+      else
+        o[i] = s[i];
+    }
+}
+
 // One block: RT 16-row tiles of W and up to 16 NT tokens.
 constexpr int MV_W = 8;  // waves
 
@@ -108,16 +120,110 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
     const int t = n * 16 + (l & 15), r = f * 16 + 4 * (l >> 4);
     if (t >= toks || r >= rows) continue;
     const sk_f32x4 s = sk_get<MV_W, RT, NT>(red, f, n, l);
-    OT* o = y + (long long)(t0 + t) * N + row0 + r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r + i < rows) {
-        if constexpr (sizeof(OT) == 2)
-          o[i] = f32_to_bf16(s[i]);
-        else
-          o[i] = s[i];
-      }
+    mv_store(y + (long long)(t0 + t) * N + row0 + r, s, rows - r);
   }
+}
+
+// Many rows and several tokens: the waves of a block take 16 RT rows each over
+// the whole K axis and share x, which passes through LDS in chunks of CH
+// steps, two buffers in turn.  (Read from L2 by every wave for itself, x costs
+// more than the weights: 65536 x 7168 rows and 16 tokens took 150, 101, 77
+// and 68 us with 1, 2, 4 and 8 row tiles to a wave.)  In LDS a fragment is 64
+// consecutive 16-byte words, the lanes' own, so its reads have no bank
+// conflicts.
+constexpr int ML_W = 8;   // waves
+constexpr int ML_D = 4;   // steps the weights' loads run ahead
+
+template <int RT, int NT, bool SV, typename OT>
+__global__ __launch_bounds__(64 * ML_W) void k_fp4_matvec_lds(const uint16_t* __restrict__ x,
+                                                              const uint8_t* __restrict__ q,
+                                                              const uint8_t* __restrict__ scale, int T, long long N,
+                                                              int K, OT* __restrict__ y) {
+  constexpr int D = ML_D, CH = 8 / NT;
+  using S = Skinny<MOE_E2M1, uint16_t, RT, NT, SV>;
+  constexpr int FRAGS = CH * NT * S::XV, MINE = FRAGS / ML_W;  // fragments of a chunk, and those that a wave stages
+  static_assert(FRAGS % ML_W == 0 && CH % D == 0, "chunks are staged by all waves, and are turns of the ring");
+  __shared__ sk_u32x4 lds[2][FRAGS][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long row0 = ((long long)blockIdx.x * ML_W + wave) * (16 * RT);
+  const int rows = (int)(row0 >= N ? 0 : N - row0 < 16 * RT ? N - row0 : 16 * RT);
+  const int t0 = blockIdx.y * (16 * NT);
+  const int toks = T - t0 < 16 * NT ? T - t0 : 16 * NT;
+  typename S::Lanes L;
+  L.K = K;
+  L.g = lane >> 4;
+  L.rw = sk_rsrc(q + row0 * (K / 2), (uint32_t)rows * (uint32_t)(K / 2));
+  L.rs = sk_rsrc(scale + row0 * (K / 32), (uint32_t)rows * (uint32_t)(K / 32));
+  L.rx = sk_rsrc(x + (long long)t0 * K, (uint32_t)toks * (uint32_t)K * 2u);
+#pragma unroll
+  for (int f = 0; f < RT; ++f) {
+    const int r = f * 16 + (lane & 15);
+    L.w_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 2) + L.g * 16u : SK_OOB;
+    L.s_off[f] = r < rows ? (uint32_t)r * (uint32_t)(K / 32) + (SV ? 0 : L.g) : SK_OOB;
+  }
+  const int steps = (K + S::STEP - 1) / S::STEP, chunks = (steps + CH - 1) / CH;
+  // fragment i of a chunk: step i / (NT XV), token tile, 16 bytes of the lane's 64
+  sk_u32x4 stage[MINE];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+      const int i = wave * MINE + m;
+      const int t = i / S::XV % NT * 16 + (lane & 15), k = (c * CH + i / (NT * S::XV)) * S::STEP + L.g * S::EPL;
+      const uint32_t off = t < toks && k < K ? ((uint32_t)t * (uint32_t)K + (uint32_t)k) * 2u : SK_OOB;
+      stage[m] = __builtin_amdgcn_raw_buffer_load_b128(L.rx, off, i % S::XV * 16, 0);
+    }
+  };
+  auto put = [&](int c) {
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) lds[c & 1][wave * MINE + m][lane] = stage[m];
+    // the LDS writes alone are waited for: the loads in flight stay so
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+  };
+  sk_f32x4 acc[RT][NT];
+#pragma unroll
+  for (int f = 0; f < RT; ++f)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[f][n] = sk_f32x4{0.f, 0.f, 0.f, 0.f};
+  typename S::Step st[D];
+  typename S::Scales sc[2];
+  fetch(0);
+  if (SV) S::load_scales(sc[0], L, 0);
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    S::load_w(st[i], L, i);  // past the last step: nothing is fetched
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  put(0);
+  for (int c = 0; c < chunks; ++c) {
+    if (c + 1 < chunks) fetch(c + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int s = c * CH + i;
+      if (SV && i % 4 == 0) S::load_scales(sc[1], L, s + 4);
+      if (s < steps) {  // past it the exponent bytes are the next row's
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int v = 0; v < S::XV; ++v) st[i % D].x[n][0][v] = lds[c & 1][(i * NT + n) * S::XV + v][lane];
+        S::mma(acc, st[i % D], L, sc[0], i % 4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      S::load_w(st[i % D], L, s + D);
+      __builtin_amdgcn_sched_barrier(0);
+      if (SV && i % 4 == 3) sc[0] = sc[1];
+    }
+    if (c + 1 < chunks) put(c + 1);
+  }
+#pragma unroll
+  for (int f = 0; f < RT; ++f)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int t = n * 16 + (lane & 15), r = f * 16 + 4 * L.g;
+      if (t >= toks || r >= rows) continue;
+      mv_store(y + (long long)(t0 + t) * N + row0 + r, acc[f][n], rows - r);
+    }
 }
 
 constexpr int MV_MAX_K = 1 << 20;  // 64 rows and 32 tokens of it stay within 32-bit offsets
@@ -177,21 +283,39 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
   MOE_REQUIRE(ws_bytes >= fp4_matvec_workspace_bytes(T, N, K), MOE_EWORKSPACE,
               "workspace smaller than fp4_matvec_workspace_bytes");
   hipStream_t st = as_stream(stream);
-  auto go = [&](auto kernel, int rt, int nt, auto* out) {
-    const dim3 grid((unsigned)ceil_div(N, 16 * rt), (unsigned)ceil_div(T, 16 * nt));
-    hipLaunchKernelGGL(kernel, grid, dim3(64 * MV_W), 0, st, static_cast<const uint16_t*>(x), q, scale, T, N, K, out);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  // rows, tokens of a block
+  auto go = [&](auto kernel, int waves, int rows, int tokens, auto* out) {
+    const dim3 grid((unsigned)ceil_div(N, rows), (unsigned)ceil_div(T, tokens));
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, xb, q, scale, T, N, K, out);
   };
-  auto shape = [&](auto sv, auto* out) {
+  // By the rows alone, at K = 7168 in us, 1 token / 16 / 32.  Few rows: one
+  // tile to a block, so that there are blocks enough (4096 rows: 6.6 / 11 / 17
+  // against 8.1 / 13 / 19 with two tiles).  8192: two tiles 8.9 / 13 / 19, one
+  // 9.6 / 18 / 30, four 12 / 17 / 23.  16384: four 14 / 18 / 25, two 14 / 22 /
+  // 37, through LDS 18 / 23 / 32.  32768: LDS 30 / 34 / 43, four 29 / 40 / 55.
+  // 65536: LDS, two tiles to a wave 54 / 63 / 75, one 54 / 66 / 82, without
+  // LDS 60 / 81 / 108.
+  auto shape = [&](auto sv, auto nt, auto* out) {
     constexpr bool SV = decltype(sv)::value;
+    constexpr int NT = decltype(nt)::value;
     using OT = std::remove_pointer_t<decltype(out)>;
-    if (N >= 16384) {
-      if (T <= 16) go(k_fp4_matvec<4, 1, SV, OT>, 4, 1, out); else go(k_fp4_matvec<4, 2, SV, OT>, 4, 2, out);
-    } else {
-      if (T <= 16) go(k_fp4_matvec<1, 1, SV, OT>, 1, 1, out); else go(k_fp4_matvec<1, 2, SV, OT>, 1, 2, out);
-    }
+    if (N >= 65536)
+      go(k_fp4_matvec_lds<2, NT, SV, OT>, ML_W, 32 * ML_W, 16 * NT, out);
+    else if (N >= 24576)
+      go(k_fp4_matvec_lds<1, NT, SV, OT>, ML_W, 16 * ML_W, 16 * NT, out);
+    else if (N >= 12288)
+      go(k_fp4_matvec<4, NT, SV, OT>, MV_W, 64, 16 * NT, out);
+    else if (N >= 6144)
+      go(k_fp4_matvec<2, NT, SV, OT>, MV_W, 32, 16 * NT, out);
+    else
+      go(k_fp4_matvec<1, NT, SV, OT>, MV_W, 16, 16 * NT, out);
+  };
+  auto tokens = [&](auto sv, auto* out) {
+    if (T <= 16) shape(sv, std::integral_constant<int, 1>{}, out); else shape(sv, std::integral_constant<int, 2>{}, out);
   };
   auto pick = [&](auto* out) {
-    if (K % 128 == 0) shape(std::true_type{}, out); else shape(std::false_type{}, out);
+    if (K % 128 == 0) tokens(std::true_type{}, out); else tokens(std::false_type{}, out);
   };
   if (y_t == MOE_BF16) pick(static_cast<uint16_t*>(y)); else pick(static_cast<float*>(y));
   return launch_status("fp4_matvec");

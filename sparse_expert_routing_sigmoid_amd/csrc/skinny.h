@@ -102,26 +102,18 @@ struct Skinny {
     for (int f = 0; f < RT; ++f) sc.v[f] = __builtin_amdgcn_raw_buffer_load_b128(L.rs, L.s_off[f], (uint32_t)s * 4u, 0);
   }
 
-  __device__ static __forceinline__ void load(Step& st, const Lanes& L, int s) {
+  __device__ static __forceinline__ uint32_t past_k(const Lanes& L, int c) {
+    return (c + L.g) * EPL < L.K ? 0u : SK_OOB;
+  }
+
+  __device__ static __forceinline__ void load_w(Step& st, const Lanes& L, int s) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
       const uint32_t c = (uint32_t)(s * LD + l) * 4u;  // first chunk of this load
-      const uint32_t oob = (int)(c + L.g) * EPL < L.K ? 0u : SK_OOB;
+      const uint32_t oob = past_k(L, (int)c);
 #pragma unroll
       for (int f = 0; f < RT; ++f)
         st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, 0);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t xo = L.x_off[n] | oob;
-        if (XBYTES < 16) {
-          const sk_u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(L.rx, xo, c * XBYTES, 0);
-          st.x[n][l][0] = sk_u32x4{v[0], v[1], 0u, 0u};
-        } else {
-#pragma unroll
-          for (int v = 0; v < XV; ++v)
-            st.x[n][l][v] = __builtin_amdgcn_raw_buffer_load_b128(L.rx, xo, c * XBYTES + v * 16u, 0);
-        }
-      }
       if (WT == MOE_E2M1 && !SV) {
 #pragma unroll
         for (int f = 0; f < RT; ++f) st.s[f] = __builtin_amdgcn_raw_buffer_load_b8(L.rs, L.s_off[f] | oob, c, 0);
@@ -132,6 +124,31 @@ struct Skinny {
       st.blk[0] = L.blk_lo[b];
       st.blk[1] = L.blk_hi[b];
     }
+  }
+
+  __device__ static __forceinline__ void load_x(sk_u32x4 (&x)[NT][LD][XV], const Lanes& L, int s) {
+#pragma unroll
+    for (int l = 0; l < LD; ++l) {
+      const uint32_t c = (uint32_t)(s * LD + l) * 4u;
+      const uint32_t oob = past_k(L, (int)c);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t xo = L.x_off[n] | oob;
+        if (XBYTES < 16) {
+          const sk_u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(L.rx, xo, c * XBYTES, 0);
+          x[n][l][0] = sk_u32x4{v[0], v[1], 0u, 0u};
+        } else {
+#pragma unroll
+          for (int v = 0; v < XV; ++v)
+            x[n][l][v] = __builtin_amdgcn_raw_buffer_load_b128(L.rx, xo, c * XBYTES + v * 16u, 0);
+        }
+      }
+    }
+  }
+
+  __device__ static __forceinline__ void load(Step& st, const Lanes& L, int s) {
+    load_w(st, L, s);
+    load_x(st.x, L, s);
   }
 
   __device__ static __forceinline__ void mma(sk_f32x4 (&acc)[RT][NT], const Step& st, const Lanes& L, const Scales& sv,

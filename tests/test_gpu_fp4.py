@@ -103,8 +103,9 @@ def test_matvec(T, N, K, yt):
 
 
 @pytest.mark.parametrize("T", [1, 16, 31])
-def test_matvec_many_rows(T):
-    N, K = 16390, 288
+@pytest.mark.parametrize("N,K", [(8200, 384), (16390, 288), (16390, 640), (24580, 1152), (30001, 1056), (65540, 288),
+                                 (65537, 2176)])
+def test_matvec_many_rows(T, N, K):
     x = W.make_free((T, K), 1.0, T, "cuda", BF16)
     q, s = codes(N, K, T)
     y = torch.empty((T, N), device="cuda")
@@ -140,6 +141,21 @@ def test_nan_stays_in_its_row_and_token():
     n = [i for i in range(N) if i != 33]
     assert torch.equal(y0[t][:, n], y1[t][:, n])
     assert torch.isnan(y1[4]).all() and torch.isnan(y1[:, 33]).all() and not torch.isfinite(y1[17]).any()
+
+
+@pytest.mark.parametrize("N", [100, 24576, 65600])
+@pytest.mark.parametrize("K", [1152, 1056, 128])
+def test_nan_scales_of_the_next_row(N, K):
+    """A row whose first groups are NaN, behind a row that ends inside a block's turn of K."""
+    T = 3
+    x = W.make_free((T, K), 1.0, 18, "cuda", BF16)
+    q, s = codes(N, K, 19)
+    y0, y1 = (torch.empty((T, N), device="cuda") for _ in range(2))
+    M.fp4_matvec(x, q, s, y0)
+    s[34], s[N - 1] = 255, 255
+    M.fp4_matvec(x, q, s, y1)
+    keep = [i for i in range(N) if i not in (34, N - 1)]
+    assert torch.equal(y0[:, keep], y1[:, keep]) and torch.isnan(y1[:, 34]).all() and torch.isnan(y1[:, N - 1]).all()
 
 
 def test_past_32_bit_offsets():
