@@ -20,7 +20,7 @@ constexpr int NORM_MAX_D = 1024 * 4 * 8;
 
 template <int TPR>
 constexpr int norm_threads() {
-  return TPR < 256 ? 256 : TPR;
+  return TPR == 64 ? 256 : TPR;
 }
 
 // Sum of v over the TPR threads of a row.  `red` holds one value per wave for
@@ -128,9 +128,10 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm(
   }
 }
 
-// dx of every row, and this row group's part of dw: rows first, first +
-// groups, ... are added in that order in registers, the row groups later in
-// the order of their number (k_norm_dw), so dw is bitwise reproducible.
+// dx of every row, and this block's part of dw: each row group (the threads
+// that share a row) adds rows group, group + groups, ... in registers, a
+// block's groups are added through LDS and the blocks by k_norm_dw, all in the
+// order of their number, so dw is bitwise reproducible.
 template <typename GT, typename RT, int TPR, int C>
 __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
     const GT* du, const RT* r, const void* __restrict__ w, bool w_bf16, const float* __restrict__ rstd, const RT* dr,
@@ -197,105 +198,113 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
         Vec8<RT>::store(dx + o + col[j], out);
       }
   }
+  if constexpr (RPB > 1) {
+    __shared__ float sum[RPB - 1][C * TPR * 8];
+    const int g = threadIdx.x / TPR;
+    if (g > 0)
+#pragma unroll
+      for (int j = 0; j < C; ++j) Vec8<float>::store(&sum[g - 1][(j * TPR + tid) * 8], dw[j]);
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int o = 0; o < RPB - 1; ++o)
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        float t[8];
+        Vec8<float>::load(&sum[o][(j * TPR + tid) * 8], t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] += t[i];
+      }
+  }
 #pragma unroll
   for (int j = 0; j < C; ++j)
-    if (live[j]) Vec8<float>::store(part + group * d + col[j], dw[j]);
+    if (live[j]) Vec8<float>::store(part + (long long)blockIdx.x * d + col[j], dw[j]);
 }
 
-// dw[j] = sum over the groups of part[., j].  A block owns 64 columns; its
-// wave w adds groups w, w + 16, ... and wave 0 adds the waves' sums in order.
-__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part, int groups, int d,
-                                                  float* __restrict__ dw) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+// dw[j] = sum over the blocks of part[., j].  A block owns 16 columns; its
+// threads r of each column add parts r, r + 16, ... and one adds their sums.
+// (64 columns and 16 waves to a block left 32 blocks at d = 2048: 38 us.)
+__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int parts, int d,
+                                                 float* __restrict__ dw) {
+  __shared__ float red[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;
   float s = 0.f;
-  if (col < d)
-    for (int g = wave; g < groups; g += 16) s += part[(long long)g * d + col];
-  red[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && col < d) {
+  if (col < d) {
+    const float* p = part + (long long)r * d + col;
+    int g = r;
+    for (; g + 7 * 16 < parts; g += 8 * 16, p += 8 * 16 * (long long)d) {
+      float v[8];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += red[i][lane];
+      for (int i = 0; i < 8; ++i) v[i] = p[i * 16 * (long long)d];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; g < parts; g += 16, p += 16 * (long long)d) s += *p;
+  }
+  red[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < d) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += red[i][c];
     dw[col] = s;
   }
 }
 
-// Threads a row is shared by and chunks a thread holds, by the row's length.
-struct NormShape {
-  int tpr, chunks;
-};
-NormShape norm_shape(int d) {
-  if (d <= 512) return {64, 1};
-  if (d <= 2048) return {64, 4};
-  if (d <= 8192) return {256, 4};
-  return {1024, 4};
-}
-
-int norm_cus() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    cus = 256;
-  return cus;
-}
-
-// Blocks of the backward: each leaves one row of dw sums per row group.
+// Blocks of the backward: each leaves one row of dw sums (8192 rows of 7168
+// bf16: 256 blocks 102 us, 512 89, 768 97, 2048 101).
 int norm_bwd_blocks(long long T, int d) {
-  const NormShape s = norm_shape(d);
-  const int rpb = s.tpr < 256 ? 256 / s.tpr : 1;
-  const long long need = ceil_div(T, rpb);
-  const long long cap = 512;
-  return (int)(need < cap ? need : cap);
+  const long long need = d <= 512 ? ceil_div(T, 4) : T;
+  return (int)(need < 512 ? need : 512);
 }
 
 bool is_fp(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
 
+// The fewest chunks a thread: every load of a row is then in flight at once
+// and few registers let many rows be resident (16384 rows of 7168 bf16 with
+// tiles: 1024 threads x 1 chunk 186 us, 512 x 2 194, 256 x 4 205; one row 2.9,
+// 3.2, 4.0).  A block a row: rows taken in a loop of 2048 blocks 214 us.
 template <typename XT, typename RT>
 void launch_norm(const void* x, const void* resid, const void* w, bool w_bf16, float eps, long long T, int d,
                  void* r_out, void* u, bool u_bf16, uint8_t* q, float* q_scale, float* rstd, hipStream_t st) {
-  const NormShape s = norm_shape(d);
-  const int threads = s.tpr < 256 ? 256 : s.tpr, rpb = threads / s.tpr;
-  const long long need = ceil_div(T, rpb);
-  const long long cap = (long long)norm_cus() * 8;
-  const dim3 grid((unsigned)(need < cap ? need : cap));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, static_cast<const XT*>(x), static_cast<const RT*>(resid), w,
-                       w_bf16, eps, T, d, static_cast<RT*>(r_out), u, u_bf16, q, q_scale, rstd);
+  auto go = [&](auto kernel, int threads, int rows) {
+    const long long need = ceil_div(T, rows), most = 1LL << 30;  // further rows in a loop
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, st,
+                       static_cast<const XT*>(x), static_cast<const RT*>(resid), w, w_bf16, eps, T, d,
+                       static_cast<RT*>(r_out), u, u_bf16, q, q_scale, rstd);
   };
-  if (s.tpr == 64 && s.chunks == 1)
-    go(k_rmsnorm<XT, RT, 64, 1>);
-  else if (s.tpr == 64)
-    go(k_rmsnorm<XT, RT, 64, 4>);
-  else if (s.tpr == 256)
-    go(k_rmsnorm<XT, RT, 256, 4>);
+  if (d <= 512)
+    go(k_rmsnorm<XT, RT, 64, 1>, 256, 4);
+  else if (d <= 2048)
+    go(k_rmsnorm<XT, RT, 256, 1>, 256, 1);
+  else if (d <= 4096)
+    go(k_rmsnorm<XT, RT, 512, 1>, 512, 1);
+  else if (d <= 8192)
+    go(k_rmsnorm<XT, RT, 1024, 1>, 1024, 1);
   else
-    go(k_rmsnorm<XT, RT, 1024, 4>);
+    go(k_rmsnorm<XT, RT, 1024, 4>, 1024, 1);
 }
 
+// The backward's blocks take rows in a loop, with dw in registers: more
+// chunks a thread keep the rows' latencies apart (8192 rows of 7168 bf16: 256
+// threads x 4 chunks 89 us, 1024 x 1 97, 512 x 2 98; 4096 rows of 2048, 256 x
+// 1 24, 64 x 4 27).
 template <typename GT, typename RT>
 void launch_norm_bwd(const void* du, const void* r, const void* w, bool w_bf16, const float* rstd, const void* dr,
                      long long T, int d, void* dx, float* part, hipStream_t st) {
-  const NormShape s = norm_shape(d);
-  const int threads = s.tpr < 256 ? 256 : s.tpr;
-  const dim3 grid(norm_bwd_blocks(T, d));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, static_cast<const GT*>(du), static_cast<const RT*>(r), w,
-                       w_bf16, rstd, static_cast<const RT*>(dr), T, d, static_cast<RT*>(dx), part);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(norm_bwd_blocks(T, d)), dim3(threads), 0, st, static_cast<const GT*>(du),
+                       static_cast<const RT*>(r), w, w_bf16, rstd, static_cast<const RT*>(dr), T, d,
+                       static_cast<RT*>(dx), part);
   };
-  if (s.tpr == 64 && s.chunks == 1)
-    go(k_rmsnorm_bwd<GT, RT, 64, 1>);
-  else if (s.tpr == 64)
-    go(k_rmsnorm_bwd<GT, RT, 64, 4>);
-  else if (s.tpr == 256)
-    go(k_rmsnorm_bwd<GT, RT, 256, 4>);
+  if (d <= 512)
+    go(k_rmsnorm_bwd<GT, RT, 64, 1>, 256);
+  else if (d <= 2048)
+    go(k_rmsnorm_bwd<GT, RT, 256, 1>, 256);
+  else if (d <= 8192)
+    go(k_rmsnorm_bwd<GT, RT, 256, 4>, 256);
   else
-    go(k_rmsnorm_bwd<GT, RT, 1024, 4>);
-}
-
-int norm_bwd_groups(long long T, int d) {
-  const NormShape s = norm_shape(d);
-  return norm_bwd_blocks(T, d) * (s.tpr < 256 ? 256 / s.tpr : 1);
+    go(k_rmsnorm_bwd<GT, RT, 1024, 4>, 1024);
 }
 
 bool norm_d_ok(int d) { return d >= 8 && d % 8 == 0 && d <= NORM_MAX_D; }
@@ -334,7 +343,7 @@ moe_status rmsnorm(const void* x, moe_dtype x_t, const void* resid, moe_dtype r_
 
 size_t rmsnorm_backward_workspace_bytes(long long T, int d) {
   if (T <= 0 || !norm_d_ok(d)) return 0;
-  return (size_t)norm_bwd_groups(T, d) * d * sizeof(float);
+  return (size_t)norm_bwd_blocks(T, d) * d * sizeof(float);
 }
 
 moe_status rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_dtype r_t, const void* w, moe_dtype w_t,
@@ -361,7 +370,7 @@ moe_status rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, moe_d
     }
   }
   // T == 0: no groups, dw = 0
-  hipLaunchKernelGGL(k_norm_dw, dim3((d + 63) / 64), dim3(1024), 0, st, part, T > 0 ? norm_bwd_groups(T, d) : 0, d, dw);
+  hipLaunchKernelGGL(k_norm_dw, dim3((d + 15) / 16), dim3(256), 0, st, part, T > 0 ? norm_bwd_blocks(T, d) : 0, d, dw);
   return launch_status("moe_rmsnorm_backward");
 }
 
