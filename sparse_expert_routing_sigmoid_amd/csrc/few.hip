@@ -348,15 +348,14 @@ __device__ __forceinline__ void few_select(const FewArgs& A, FewSelect& S, int t
 // One item: 16 RT weight rows of one expert (gate/up: 8 RT gate rows and the
 // up rows of the same columns of h) on up to 16 of its tokens, j0 and on.
 // p: token and slot of the lane's token column.
-template <int WT, typename XT, bool UP, bool SV, int W>
+template <int WT, typename XT, bool UP, bool SV, int W, bool PK>
 __device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, int j0, int p, int col0,
                                             sk_f32x4* red, int tid) {
   constexpr int RT = FEW_RT;
-  using S = Skinny<WT, XT, RT, 1, SV>;
+  using S = Skinny<WT, XT, RT, 1, SV, PK>;
   const int Kd = UP ? A.d : A.I, Nd = UP ? A.I : A.d;
   const int lane = tid & 63, wave = tid >> 6;
   const int R = A.K + A.Ns;  // h and y rows of a token
-  const int t = p >> 16, hr = t * R + (p & 0xFFFF);
   const int wrows = UP ? 2 * Nd : Nd;
   const uint32_t row_bytes = (uint32_t)sk_row_bytes(WT, Kd);
   const void* scale = UP ? A.w13_scale : A.w2_scale;
@@ -382,20 +381,33 @@ __device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, 
     L.w_off[f] = c < Nd ? r * row_bytes + L.g * 16u : SK_OOB;
     L.s_off[f] = c < Nd ? r * s_row + (SV ? 0 : L.g) : SK_OOB;
   }
-  L.x_off[0] = j0 + (lane & 15) < toks ? (uint32_t)(UP ? t : hr) * (uint32_t)Kd * (uint32_t)sizeof(XT) +
-                                             L.g * (uint32_t)S::XBYTES
-                                       : SK_OOB;
-  sk_f32x4 acc[RT][1];
+  const int j = PK ? (lane & 15) / S::XV : lane & 15;  // the token whose x the lane reads
+  const int px = PK ? __shfl(p, j, 64) : p;
+  const uint32_t x_row = (uint32_t)(UP ? px >> 16 : (px >> 16) * R + (px & 0xFFFF));
+  L.x_off[0] = j0 + j < toks ? x_row * (uint32_t)Kd * (uint32_t)sizeof(XT) + L.g * (uint32_t)S::XBYTES +
+                                   (PK ? (uint32_t)(lane % S::XV) * 16u : 0u)
+                             : SK_OOB;
+  sk_f32x4 acc[RT][S::AC];
   S::template run_part<FEW_D>(acc, L, 0, (Kd + S::STEP - 1) / S::STEP, wave, W);
-  sk_put<RT, 1>(red, acc, tid);
+  if constexpr (PK)
+    sk_put_packed<RT, S::XV>(red, acc, tid);
+  else
+    sk_put<RT, 1>(red, acc, tid);
+  auto sum = [&](int f) {
+    if constexpr (PK)
+      return sk_get_packed<W, RT, S::XV>(red, f, lane);
+    else
+      return sk_get<W, RT, 1>(red, f, 0, lane);
+  };
+  const int hr = (p >> 16) * R + (p & 0xFFFF);  // row of h or y of the lane's token
   constexpr int OUT_TILES = UP ? RT / 2 : RT;
   for (int i = tid; i < OUT_TILES * 64; i += 64 * W) {
     const int f = i >> 6, c = col0 + f * 16 + 4 * L.g;  // 64 threads to a tile: each its own lane's column
     if (j0 + (lane & 15) >= toks || c >= Nd) continue;  // Nd % 4 == 0: four columns exist or none
     const long long o = (long long)hr * Nd + c;
-    const sk_f32x4 a = sk_get<W, RT, 1>(red, f, 0, lane);
+    const sk_f32x4 a = sum(f);
     if constexpr (UP) {
-      const sk_f32x4 b = sk_get<W, RT, 1>(red, f + RT / 2, 0, lane);
+      const sk_f32x4 b = sum(f + RT / 2);
       float v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = silu(a[q]) * b[q];
@@ -454,17 +466,19 @@ __device__ __forceinline__ void few_combine(const FewArgs& A, int col0, int tid)
   }
 }
 
-// An expert's column tile on all its tokens.  More than 16: the rows are read
-// again, from a cache that has just held them.
-template <int WT, typename XT, bool UP, bool SV, int W>
+// An expert's column tile on all its tokens, as many at a time as the form
+// takes; the rows are read again from a cache that has just held them.
+template <int WT, typename XT, bool UP, bool SV, bool PK, int W>
 __device__ __forceinline__ void few_item(const FewArgs& A, int ex, int toks, const int32_t* pairs, int p, int col0,
                                          sk_f32x4* red, int tid) {
-  for (int j0 = 0; j0 < toks; j0 += 16) {
+  constexpr int TOKENS = Skinny<WT, XT, FEW_RT, 1, SV, PK>::TOKENS;
+  for (int j0 = 0; j0 < toks; j0 += TOKENS) {
     if (j0) {
-      p = pairs ? pairs[j0 + (tid & 15)] : p + (16 << 16);
+      const int j = j0 + (tid & 15);
+      p = !pairs ? p + (TOKENS << 16) : pairs[j < FEW_T ? j : FEW_T - 1];
       __syncthreads();  // red is read until here
     }
-    few_product<WT, XT, UP, SV, W>(A, ex, toks, j0, p, col0, red, tid);
+    few_product<WT, XT, UP, SV, W, PK>(A, ex, toks, j0, p, col0, red, tid);
   }
 }
 
@@ -472,7 +486,7 @@ constexpr int FEW_UP_COLS = FEW_RT * 8, FEW_DOWN_COLS = FEW_RT * 16;  // columns
 
 // Block 0 selects; the others are the shared experts' gate/up, with many
 // waves to a block: they are alone on the chip.
-template <int WT, typename XT, bool SV>
+template <int WT, typename XT, bool SV, bool PK>
 __global__ __launch_bounds__(64 * SELECT_W) void k_few_select(FewArgs A) {
   __shared__ union {
     sk_f32x4 red[SELECT_W * FEW_RT * 64];
@@ -485,12 +499,12 @@ __global__ __launch_bounds__(64 * SELECT_W) void k_few_select(FewArgs A) {
   }
   const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS;
   const int item = blockIdx.x - 1, e = item / tiles;
-  few_item<WT, XT, true, SV, SELECT_W>(A, A.Nr + e, A.T, nullptr, (tid & 15) << 16 | (A.K + e), (item % tiles) * FEW_UP_COLS,
+  few_item<WT, XT, true, SV, PK, SELECT_W>(A, A.Nr + e, A.T, nullptr, (tid & 15) << 16 | (A.K + e), (item % tiles) * FEW_UP_COLS,
                              lds.red, tid);
 }
 
-template <int WT, typename XT, bool SV>
-__global__ __launch_bounds__(FEW_THREADS) void k_few_up(FewArgs A) {
+template <int WT, typename XT, bool SV, bool PK>
+__global__ __launch_bounds__(FEW_THREADS, PK ? 4 : 1) void k_few_up(FewArgs A) {
   __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
   const int tid = threadIdx.x;
   const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, e = blockIdx.x / tiles;
@@ -499,11 +513,11 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few_up(FewArgs A) {
   const int32_t* pairs = A.lists.pair + e * FEW_T;
   const int p = pairs[tid & 15];
   if (e >= n) return;
-  few_item<WT, XT, true, SV, FEW_W>(A, ex, toks, pairs, p, (blockIdx.x % tiles) * FEW_UP_COLS, red, tid);
+  few_item<WT, XT, true, SV, PK, FEW_W>(A, ex, toks, pairs, p, (blockIdx.x % tiles) * FEW_UP_COLS, red, tid);
 }
 
-template <int WT, typename XT, bool SV>
-__global__ __launch_bounds__(FEW_THREADS) void k_few_down(FewArgs A) {
+template <int WT, typename XT, bool SV, bool PK>
+__global__ __launch_bounds__(FEW_THREADS, PK ? 4 : 1) void k_few_down(FewArgs A) {
   __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
   __shared__ uint32_t s_count;
   const int tid = threadIdx.x;
@@ -518,19 +532,37 @@ __global__ __launch_bounds__(FEW_THREADS) void k_few_down(FewArgs A) {
     p = pairs[tid & 15];
     if (e - A.Ns >= n) return;
   }
-  few_item<WT, XT, false, SV, FEW_W>(A, ex, toks, pairs, p, tile * FEW_DOWN_COLS, red, tid);
+  few_item<WT, XT, false, SV, PK, FEW_W>(A, ex, toks, pairs, p, tile * FEW_DOWN_COLS, red, tid);
   if (few_signal(A.column_done + tile * FEW_LINE, &s_count, tid) == (uint32_t)(A.Ns + n) - 1)
     few_combine(A, tile * FEW_DOWN_COLS, tid);
 }
 
+// Packed where an expert has few tokens: at most two for every routed expert
+// on average, or no more tokens than fit.  (d = 7168, 256 experts, whole
+// layer: E4M3, 32 tokens, 1285 us against 1330; 4-bit, one token, 66 against
+// 69, with the registers held to four waves a SIMD, else 71.)  With more
+// tokens an expert the repeated reading of its rows would cost more than the
+// loads of x that it saves.
 template <int WT, typename XT, bool SV>
 void launch_blocks(const FewArgs& A, hipStream_t st) {
+  constexpr bool NARROW = WT == MOE_E4M3 || WT == MOE_E2M1;
+  constexpr int PACKED = Skinny<WT, XT, FEW_RT, 1, SV, NARROW>::TOKENS;
   const int touched = A.T * A.K < A.Nr ? A.T * A.K : A.Nr;
   const int up = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, down = (A.d + FEW_DOWN_COLS - 1) / FEW_DOWN_COLS;
   const dim3 block(FEW_THREADS);
-  hipLaunchKernelGGL((k_few_select<WT, XT, SV>), dim3(1 + A.Ns * up), dim3(64 * SELECT_W), 0, st, A);
-  hipLaunchKernelGGL((k_few_up<WT, XT, SV>), dim3(touched * up), block, 0, st, A);
-  hipLaunchKernelGGL((k_few_down<WT, XT, SV>), dim3((touched + A.Ns) * down), block, 0, st, A);
+  auto select = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1 + A.Ns * up), dim3(64 * SELECT_W), 0, st, A); };
+  auto products = [&](auto k_up, auto k_down) {
+    hipLaunchKernelGGL(k_up, dim3(touched * up), block, 0, st, A);
+    hipLaunchKernelGGL(k_down, dim3((touched + A.Ns) * down), block, 0, st, A);
+  };
+  if (NARROW && A.T <= PACKED)
+    select(k_few_select<WT, XT, SV, NARROW>);
+  else
+    select(k_few_select<WT, XT, SV, false>);
+  if (NARROW && (A.T <= PACKED || A.T * A.K <= 2 * A.Nr))
+    products(k_few_up<WT, XT, SV, NARROW>, k_few_down<WT, XT, SV, NARROW>);
+  else
+    products(k_few_up<WT, XT, SV, false>, k_few_down<WT, XT, SV, false>);
 }
 
 template <int WT, typename XT>

@@ -16,6 +16,15 @@
 // zeros on both sides, as do rows and tokens that do not exist, so nothing is
 // read out of bounds and a NaN in one row or token stays in its own results.
 //
+// Few tokens of a narrow type.  A chunk of E4M3 or E2M1 weights meets 32 or 64
+// bytes of x, XV loads of 16 bytes a lane, of which one token fills only the
+// lanes of one column: x then costs more load instructions than the weights.
+// Packed (PK), up to 16 / XV tokens share one load: column t XV + v holds
+// piece v of token t, the products of the weights' piece v go to accumulator
+// v, and the sum of a token is that of its XV columns, column t XV + v taken
+// from accumulator v.  What the other columns of an accumulator hold is not
+// used.
+//
 // Weight types: fp32 (fp32 matrix instructions); bf16; E4M3 with one scale
 // per 128x128 block; E2M1 with one exponent byte per 32 columns of a row,
 // exactly one lane's chunk.  The two narrow types are widened to bf16 by the
@@ -69,27 +78,31 @@ __device__ __forceinline__ sk_bf16x8 sk_join(sk_bf16x2 a, sk_bf16x2 b, sk_bf16x2
 // SV: the exponent bytes of E2M1 weights are read 16 at a time, four steps'
 // worth of a row's, which needs rows of a multiple of 4 bytes (K % 128 == 0);
 // otherwise a byte a step.
-template <int WT, typename XT, int RT, int NT, bool SV = false>
+template <int WT, typename XT, int RT, int NT, bool SV = false, bool PK = false>
 struct Skinny {
   static_assert(!SV || WT == MOE_E2M1, "only E2M1 has exponent bytes");
   static constexpr int EPL = SkinnyWeight<WT>::EPL, LD = SkinnyWeight<WT>::LD;
   static constexpr int STEP = 4 * EPL * LD;                             // K indices per step
   static constexpr int XBYTES = EPL * (int)sizeof(XT);                  // x bytes of a chunk: 8, 16, 32 or 64
-  static constexpr int XV = XBYTES < 16 ? 1 : XBYTES / 16;
+  static constexpr int XV = XBYTES < 16 ? 1 : XBYTES / 16;              // 16-byte pieces of it
+  static constexpr int XL = PK ? 1 : XV;                                // loads of it
+  static constexpr int AC = PK ? XV : NT;                               // accumulators of a row tile
+  static constexpr int TOKENS = PK ? 16 / XV : 16 * NT;                 // tokens at a time
+  static_assert(!PK || NT == 1, "one tile of columns");
   static_assert(WT == MOE_F32 || sizeof(XT) == 2, "narrow weights take bf16 tokens");
 
   struct Lanes {
     __amdgpu_buffer_rsrc_t rw, rs, rx;
     uint32_t w_off[RT];  // byte offset of the lane's row of tile f, chunk l / 16 included; SK_OOB: no such row
     uint32_t s_off[RT];  // E2M1: byte offset of its exponent bytes (SV: the row's, else chunk l / 16 included)
-    uint32_t x_off[NT];  // byte offset of the lane's token row, chunk l / 16 included; SK_OOB: no such token
+    uint32_t x_off[NT];  // byte offset of the lane's token row, chunk l / 16 (PK: and piece) included; SK_OOB: none
     const float* blk_lo;  // E4M3: scales along K of the 128-row block of tiles f < RT / 2, and of the others
     const float* blk_hi;
     int K, g;
   };
   struct Step {
     sk_u32x4 w[RT][LD];
-    sk_u32x4 x[NT][LD][XV];
+    sk_u32x4 x[NT][LD][XL];
     uint32_t s[RT];
     float blk[2];
   };
@@ -126,7 +139,7 @@ struct Skinny {
     }
   }
 
-  __device__ static __forceinline__ void load_x(sk_u32x4 (&x)[NT][LD][XV], const Lanes& L, int s) {
+  __device__ static __forceinline__ void load_x(sk_u32x4 (&x)[NT][LD][XL], const Lanes& L, int s) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
       const uint32_t c = (uint32_t)(s * LD + l) * 4u;
@@ -139,7 +152,7 @@ struct Skinny {
           x[n][l][0] = sk_u32x4{v[0], v[1], 0u, 0u};
         } else {
 #pragma unroll
-          for (int v = 0; v < XV; ++v)
+          for (int v = 0; v < XL; ++v)
             x[n][l][v] = __builtin_amdgcn_raw_buffer_load_b128(L.rx, xo, c * XBYTES + v * 16u, 0);
         }
       }
@@ -151,7 +164,7 @@ struct Skinny {
     load_x(st.x, L, s);
   }
 
-  __device__ static __forceinline__ void mma(sk_f32x4 (&acc)[RT][NT], const Step& st, const Lanes& L, const Scales& sv,
+  __device__ static __forceinline__ void mma(sk_f32x4 (&acc)[RT][AC], const Step& st, const Lanes& L, const Scales& sv,
                                              int i4) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
@@ -198,9 +211,11 @@ struct Skinny {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < EPL / 8; ++j)
-              acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], __builtin_bit_cast(sk_bf16x8, st.x[n][l][j]),
-                                                                  acc[f][n], 0, 0, 0);
+            for (int j = 0; j < EPL / 8; ++j) {
+              sk_f32x4& c = acc[f][PK ? j % XV : n];
+              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], __builtin_bit_cast(sk_bf16x8, st.x[n][l][PK ? 0 : j]), c,
+                                                          0, 0, 0);
+            }
         }
       }
     }
@@ -210,13 +225,13 @@ struct Skinny {
   // step past the end is loaded or multiplied (a wave has few steps, so
   // rounding their number up to D costs more than the branches).
   template <int D>
-  __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1) {
+  __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][AC], const Lanes& L, int s0, int s1) {
     constexpr int U = SV ? 4 : D;  // steps to a turn of the loop: a vector holds the exponent bytes of four
     static_assert(U % D == 0, "a turn of the loop goes round the ring");
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[f][n] = sk_f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < AC; ++n) acc[f][n] = sk_f32x4{0.f, 0.f, 0.f, 0.f};
     s0 = __builtin_amdgcn_readfirstlane(s0);
     s1 = __builtin_amdgcn_readfirstlane(s1);
     Step st[D];
@@ -251,7 +266,7 @@ struct Skinny {
 
   // Wave w of W: steps [s0, s1) cut into W runs of equal length (or one less).
   template <int D>
-  __device__ static __forceinline__ void run_part(sk_f32x4 (&acc)[RT][NT], const Lanes& L, int s0, int s1, int w, int W) {
+  __device__ static __forceinline__ void run_part(sk_f32x4 (&acc)[RT][AC], const Lanes& L, int s0, int s1, int w, int W) {
     const int n = s1 > s0 ? s1 - s0 : 0;
     run<D>(acc, L, s0 + n * w / W, s0 + n * (w + 1) / W);
   }
@@ -274,6 +289,36 @@ __device__ __forceinline__ sk_f32x4 sk_get(const sk_f32x4* red, int f, int n, in
   sk_f32x4 s = red[(f * NT + n) * 64 + lane];
 #pragma unroll
   for (int w = 1; w < W; ++w) s += red[((w * RT + f) * NT + n) * 64 + lane];
+  return s;
+}
+
+// The same for packed tokens (token lane % 16, below 16 / XV): one tile of
+// columns a wave, each from its own accumulator.
+template <int RT, int XV>
+__device__ __forceinline__ void sk_put_packed(sk_f32x4* red, const sk_f32x4 (&acc)[RT][XV], int tid) {
+  const int lane = tid & 63, wave = tid >> 6;
+#pragma unroll
+  for (int f = 0; f < RT; ++f) {
+    sk_f32x4 v = acc[f][0];
+#pragma unroll
+    for (int n = 1; n < XV; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lane % XV == n ? acc[f][n][i] : v[i];
+    red[(wave * RT + f) * 64 + lane] = v;
+  }
+  __syncthreads();
+}
+template <int W, int RT, int XV>
+__device__ __forceinline__ sk_f32x4 sk_get_packed(const sk_f32x4* red, int f, int lane) {
+  const int at = (lane & 48) + (lane & 15) * XV;
+  sk_f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    sk_f32x4 v = red[(w * RT + f) * 64 + at];
+#pragma unroll
+    for (int n = 1; n < XV; ++n) v += red[(w * RT + f) * 64 + at + n];
+    s = w ? s + v : v;
+  }
   return s;
 }
 
