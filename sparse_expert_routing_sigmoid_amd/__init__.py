@@ -666,10 +666,11 @@ class MoeLayer:
         moe_permute(self.topk_idx, self.Nr, self.Ns, self.tile_m, self.seg_offset, self.row_token, self.inv_row,
                     self.tile_map, self.n_tiles, self.perm_ws, stream)
 
-    def experts(self, u, stream=None):
+    def experts(self, u, stream=None, tiles_ready=False):
         w = self.w
         if self.x_fp8:
-            fp8_quantize_tiles(u, 1, self.xq, self.xs, stream=stream)
+            if not tiles_ready:
+                fp8_quantize_tiles(u, 1, self.xq, self.xs, stream=stream)
             x, xs = self.xq, self.xs
         else:
             x, xs = u, None
@@ -692,12 +693,13 @@ class MoeLayer:
         moe_combine(u, self.y, self.inv_row, self.topk_gate, self.seg_offset, self.Nr, self.Ns, out, flags, stream)
         return out
 
-    def experts_combine(self, u, flags=0, stream=None):
+    def experts_combine(self, u, flags=0, stream=None, tiles_ready=False):
         """Expert GEMMs with the combine fused into the down projection
         (moe_expert_gemm_combine); returns the fp32 layer output."""
         w = self.w
         if self.x_fp8:
-            fp8_quantize_tiles(u, 1, self.xq, self.xs, stream=stream)
+            if not tiles_ready:
+                fp8_quantize_tiles(u, 1, self.xq, self.xs, stream=stream)
             x, xs = self.xq, self.xs
         else:
             x, xs = u, None
@@ -707,12 +709,16 @@ class MoeLayer:
                                 x_t=self.x_t, stream=stream)
         return self.out
 
-    def forward(self, u, centroids, bias, stream=None):
+    def forward(self, u, centroids, bias, stream=None, tiles_ready=False):
+        """tiles_ready (E4M3 activations): u's 1x128 tiles are in self.xq /
+        self.xs already, written by moe_rmsnorm with u."""
+        if tiles_ready and not self.x_fp8:
+            raise ValueError("tiles_ready needs a layer with E4M3 activations (x_fp8)")
         self.route(u, centroids, bias, stream)
         self.permute(stream)
         if self.fused:
-            return self.experts_combine(u, stream=stream)
-        self.experts(u, stream)
+            return self.experts_combine(u, stream=stream, tiles_ready=tiles_ready)
+        self.experts(u, stream, tiles_ready)
         return self.combine(u, stream=stream)
 
     def backward(self, grad_out, u, centroids, stream=None):
