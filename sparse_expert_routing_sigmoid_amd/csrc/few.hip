@@ -49,7 +49,7 @@ constexpr int FEW_D = 2;    // steps a product wave's loads run ahead
 constexpr int LOGIT_W = 8;  // waves of a router block
 constexpr int FEW_THREADS = 64 * FEW_W;
 constexpr int SELECT_W = 8;   // waves of a k_few_select block
-constexpr int LOGIT_PARTS = 8;
+constexpr int LOGIT_PARTS = 16;
 // Words of a cache line: atomics of all XCDs on one line pass at 30 to 40 a
 // microsecond, so busy counters have a line each.
 constexpr int FEW_LINE = 32;
@@ -78,7 +78,7 @@ struct FewWs {
 int few_parts(int d, int Nr) {
   const int step = 4 * SkinnyWeight<MOE_F32>::EPL * SkinnyWeight<MOE_F32>::LD;
   const int tiles = (Nr + 15) / 16, steps = (d + step - 1) / step;
-  int parts = 256 / tiles;
+  int parts = 512 / tiles;
   if (parts > LOGIT_PARTS) parts = LOGIT_PARTS;
   if (parts > steps / LOGIT_W) parts = steps / LOGIT_W;
   return parts < 1 ? 1 : parts;
@@ -197,10 +197,13 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
   // branches (past Nr: expert Nr - 1), so their latencies overlap
   constexpr int AHEAD = EPL > 4 ? 1 : LOGIT_PARTS;
   int at[EPL];
+  float add[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
+    const int i = lane + 64 * j < Nr ? lane + 64 * j : Nr - 1;
     s[j] = 0.f;
-    at[j] = t * Nr + (lane + 64 * j < Nr ? lane + 64 * j : Nr - 1);
+    at[j] = t * Nr + i;
+    add[j] = bias[i];
   }
   for (int p0 = 0; p0 < parts; p0 += AHEAD) {
     float v[AHEAD][EPL];
@@ -219,7 +222,7 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
     key[j] = 0;
     s[j] = 1.0f / (1.0f + expf(-s[j]));
     if (i < Nr) {
-      key[j] = float_order_key(s[j] + bias[i]);
+      key[j] = float_order_key(s[j] + add[j]);
       avail |= 1u << j;
     }
   }

@@ -84,17 +84,17 @@ __device__ __forceinline__ void mv_store(OT* o, const sk_f32x4& s, int n) {
 // One block: RT 16-row tiles of W and up to 16 NT tokens.
 constexpr int MV_W = 8;  // waves
 
-template <int RT, int NT, bool SV, typename OT>
+template <int RT, int NT, bool SV, bool PK, typename OT>
 __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                                                           const uint8_t* __restrict__ scale, int T, long long N, int K,
                                                           OT* __restrict__ y) {
-  using S = Skinny<MOE_E2M1, uint16_t, RT, NT, SV>;
+  using S = Skinny<MOE_E2M1, uint16_t, RT, NT, SV, PK>;
   __shared__ sk_f32x4 red[MV_W * RT * NT * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long long row0 = (long long)blockIdx.x * (16 * RT);
   const int rows = (int)(N - row0 < 16 * RT ? N - row0 : 16 * RT);
-  const int t0 = blockIdx.y * (16 * NT);
-  const int toks = T - t0 < 16 * NT ? T - t0 : 16 * NT;
+  const int t0 = blockIdx.y * S::TOKENS;
+  const int toks = T - t0 < S::TOKENS ? T - t0 : S::TOKENS;
   typename S::Lanes L;
   L.K = K;
   L.g = lane >> 4;
@@ -109,17 +109,26 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int t = n * 16 + (lane & 15);
-    L.x_off[n] = t < toks ? (uint32_t)t * (uint32_t)K * 2u + L.g * (uint32_t)S::XBYTES : SK_OOB;
+    const int t = PK ? (lane & 15) / S::XV : n * 16 + (lane & 15);
+    L.x_off[n] = t < toks ? (uint32_t)t * (uint32_t)K * 2u + L.g * (uint32_t)S::XBYTES +
+                                (PK ? (uint32_t)(lane % S::XV) * 16u : 0u)
+                          : SK_OOB;
   }
-  sk_f32x4 acc[RT][NT];
+  sk_f32x4 acc[RT][S::AC];
   S::template run_part<2>(acc, L, 0, (K + S::STEP - 1) / S::STEP, wave, MV_W);
-  sk_put<RT, NT>(red, acc, threadIdx.x);
+  if constexpr (PK)
+    sk_put_packed<RT, S::XV>(red, acc, threadIdx.x);
+  else
+    sk_put<RT, NT>(red, acc, threadIdx.x);
   for (int e = threadIdx.x; e < RT * NT * 64; e += 64 * MV_W) {
     const int l = e & 63, n = (e >> 6) % NT, f = (e >> 6) / NT;
     const int t = n * 16 + (l & 15), r = f * 16 + 4 * (l >> 4);
     if (t >= toks || r >= rows) continue;
-    const sk_f32x4 s = sk_get<MV_W, RT, NT>(red, f, n, l);
+    sk_f32x4 s;
+    if constexpr (PK)
+      s = sk_get_packed<MV_W, RT, S::XV>(red, f, l);
+    else
+      s = sk_get<MV_W, RT, NT>(red, f, n, l);
     mv_store(y + (long long)(t0 + t) * N + row0 + r, s, rows - r);
   }
 }
@@ -289,33 +298,41 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     const dim3 grid((unsigned)ceil_div(N, rows), (unsigned)ceil_div(T, tokens));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, xb, q, scale, T, N, K, out);
   };
-  // By the rows alone, at K = 7168 in us, 1 token / 16 / 32.  Few rows: one
-  // tile to a block, so that there are blocks enough (4096 rows: 6.6 / 11 / 17
-  // against 8.1 / 13 / 19 with two tiles).  8192: two tiles 8.9 / 13 / 19, one
-  // 9.6 / 18 / 30, four 12 / 17 / 23.  16384: four 14 / 18 / 25, two 14 / 22 /
-  // 37, through LDS 18 / 23 / 32.  32768: LDS 30 / 34 / 43, four 29 / 40 / 55.
-  // 65536: LDS, two tiles to a wave 54 / 63 / 75, one 54 / 66 / 82, without
-  // LDS 60 / 81 / 108.
-  auto shape = [&](auto sv, auto nt, auto* out) {
+  // At K = 7168, in us.  Up to 4 tokens, packed, 1 and 4 tokens: 4096 rows 6.0
+  // / 6.1 with one row tile to a block, 7.8 / 7.9 with two (not packed 6.6 /
+  // 7.6); 16384: 12.8 / 13.3, two 13.4 / 13.4; 32768: 31 / 35, two 28 / 31;
+  // 65536: 54 / 67, two 56 / 57, through LDS 54 / 56.
+  // More tokens, 16 and 32: 4096 rows, one tile 11 / 17, two 13 / 19; 8192: two
+  // 13 / 19, one 18 / 30, four 17 / 23; 16384: four 18 / 25, two 22 / 37,
+  // through LDS 23 / 32; 32768: LDS 34 / 43, four 40 / 55; 65536: LDS, two tiles
+  // to a wave 62 / 72, one 66 / 82, without LDS 81 / 108.
+  auto shape = [&](auto sv, auto* out) {
     constexpr bool SV = decltype(sv)::value;
-    constexpr int NT = decltype(nt)::value;
     using OT = std::remove_pointer_t<decltype(out)>;
-    if (N >= 65536)
-      go(k_fp4_matvec_lds<2, NT, SV, OT>, ML_W, 32 * ML_W, 16 * NT, out);
+    auto many = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      if (N >= 65536)
+        go(k_fp4_matvec_lds<2, NT, SV, OT>, ML_W, 32 * ML_W, 16 * NT, out);
+      else if (N >= 24576)
+        go(k_fp4_matvec_lds<1, NT, SV, OT>, ML_W, 16 * ML_W, 16 * NT, out);
+      else if (N >= 12288)
+        go(k_fp4_matvec<4, NT, SV, false, OT>, MV_W, 64, 16 * NT, out);
+      else if (N >= 6144)
+        go(k_fp4_matvec<2, NT, SV, false, OT>, MV_W, 32, 16 * NT, out);
+      else
+        go(k_fp4_matvec<1, NT, SV, false, OT>, MV_W, 16, 16 * NT, out);
+    };
+    if (T > 16)
+      many(std::integral_constant<int, 2>{});
+    else if (T > 4)
+      many(std::integral_constant<int, 1>{});
     else if (N >= 24576)
-      go(k_fp4_matvec_lds<1, NT, SV, OT>, ML_W, 16 * ML_W, 16 * NT, out);
-    else if (N >= 12288)
-      go(k_fp4_matvec<4, NT, SV, OT>, MV_W, 64, 16 * NT, out);
-    else if (N >= 6144)
-      go(k_fp4_matvec<2, NT, SV, OT>, MV_W, 32, 16 * NT, out);
+      go(k_fp4_matvec<2, 1, SV, true, OT>, MV_W, 32, 4, out);
     else
-      go(k_fp4_matvec<1, NT, SV, OT>, MV_W, 16, 16 * NT, out);
-  };
-  auto tokens = [&](auto sv, auto* out) {
-    if (T <= 16) shape(sv, std::integral_constant<int, 1>{}, out); else shape(sv, std::integral_constant<int, 2>{}, out);
+      go(k_fp4_matvec<1, 1, SV, true, OT>, MV_W, 16, 4, out);
   };
   auto pick = [&](auto* out) {
-    if (K % 128 == 0) tokens(std::true_type{}, out); else tokens(std::false_type{}, out);
+    if (K % 128 == 0) shape(std::true_type{}, out); else shape(std::false_type{}, out);
   };
   if (y_t == MOE_BF16) pick(static_cast<uint16_t*>(y)); else pick(static_cast<float*>(y));
   return launch_status("fp4_matvec");
