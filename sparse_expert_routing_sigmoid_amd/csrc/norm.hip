@@ -18,6 +18,13 @@ namespace {
 
 constexpr int NORM_MAX_D = 1024 * 4 * 8;
 
+// The longest rows leave no registers for w, nor for dr ahead of its use: both
+// are then read where they are needed.
+template <int TPR, int C>
+constexpr bool norm_keeps_w() {
+  return TPR * C <= 2048;
+}
+
 template <int TPR>
 constexpr int norm_threads() {
   return TPR == 64 ? 256 : TPR;
@@ -55,14 +62,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm(
   __shared__ float red[2][16];
   constexpr int RPB = norm_threads<TPR>() / TPR;  // rows a block works on at a time
   const int tid = threadIdx.x % TPR;
+  constexpr bool KEEP = norm_keeps_w<TPR, C>();
   int col[C];
   bool live[C];
-  float wv[C][8];
+  float wv[KEEP ? C : 1][8];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     col[j] = (j * TPR + tid) * 8;
     live[j] = col[j] < d;
-    if (live[j]) load_w8(w, w_bf16, col[j], wv[j]);
+    if (KEEP && live[j]) load_w8(w, w_bf16, col[j], wv[j]);
   }
   int parity = 0;
   for (long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR; row < T; row += (long long)gridDim.x * RPB) {
@@ -101,8 +109,10 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm(
       if (live[j]) {
         if (r_out) Vec8<RT>::store(r_out + o + col[j], v[j]);
         float y[8];
+        float (&wj)[8] = wv[KEEP ? j : 0];
+        if (!KEEP) load_w8(w, w_bf16, col[j], wj);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = v[j][i] * c * wv[j][i];
+        for (int i = 0; i < 8; ++i) y[i] = v[j][i] * c * wj[i];
         if (u) {
           if (u_bf16)
             Vec8<uint16_t>::store(static_cast<uint16_t*>(u) + o + col[j], y);
@@ -140,14 +150,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
   constexpr int RPB = norm_threads<TPR>() / TPR;
   const int tid = threadIdx.x % TPR;
   const long long group = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+  constexpr bool KEEP = norm_keeps_w<TPR, C>();
   int col[C];
   bool live[C];
-  float wv[C][8], dw[C][8];
+  float wv[KEEP ? C : 1][8], dw[C][8];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     col[j] = (j * TPR + tid) * 8;
     live[j] = col[j] < d;
-    if (live[j]) load_w8(w, w_bf16, col[j], wv[j]);
+    if (KEEP && live[j]) load_w8(w, w_bf16, col[j], wv[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   }
@@ -162,20 +173,22 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
       if (live[j]) {
         rg[j].load(du + o + col[j]);
         rr[j].load(r + o + col[j]);
-        if (dr) rd[j].load(dr + o + col[j]);
+        if (KEEP && dr) rd[j].load(dr + o + col[j]);
       }
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < C; ++j)
       if (live[j]) {
         float g[8], h[8];
+        float (&wj)[8] = wv[KEEP ? j : 0];
+        if (!KEEP) load_w8(w, w_bf16, col[j], wj);
         rg[j].get(g);
         rr[j].get(h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float gx = g[i] * (h[i] * c);
           dw[j][i] += gx;
-          s = fmaf(gx, wv[j][i], s);
+          s = fmaf(gx, wj[i], s);
         }
       }
     s = row_sum<TPR>(s, red, parity);
@@ -185,12 +198,15 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void k_rmsnorm_bwd(
     for (int j = 0; j < C; ++j)
       if (live[j]) {
         float g[8], h[8], out[8];
+        float (&wj)[8] = wv[KEEP ? j : 0];
+        if (!KEEP) load_w8(w, w_bf16, col[j], wj);
         rg[j].get(g);
         rr[j].get(h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = c * (g[i] * wv[j][i] - h[i] * c * m);
+        for (int i = 0; i < 8; ++i) out[i] = c * (g[i] * wj[i] - h[i] * c * m);
         if (dr) {
           float t[8];
+          if (!KEEP) rd[j].load(dr + o + col[j]);
           rd[j].get(t);
 #pragma unroll
           for (int i = 0; i < 8; ++i) out[i] += t[i];
@@ -251,11 +267,14 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
   }
 }
 
-// Blocks of the backward: each leaves one row of dw sums (8192 rows of 7168
-// bf16: 256 blocks 102 us, 512 89, 768 97, 2048 101).
+// Blocks of the backward: each leaves one row of dw sums, so few are wanted,
+// and enough rows under way to cover the latency (bf16, 117M values: d = 264,
+// 512 blocks 248 us, 1024 165, 2048 192; d = 1024, 512 blocks 141, 1024 147; d
+// = 2048, 512 blocks 164, 1024 143; d = 7168, 256 blocks 102, 512 89, 768 97
+// for half as many).
 int norm_bwd_blocks(long long T, int d) {
-  const long long need = d <= 512 ? ceil_div(T, 4) : T;
-  return (int)(need < 512 ? need : 512);
+  const long long need = d <= 1024 ? ceil_div(T, 4) : T, most = d <= 512 || (d > 1024 && d <= 2048) ? 1024 : 512;
+  return (int)(need < most ? need : most);
 }
 
 bool is_fp(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16; }
@@ -281,6 +300,8 @@ void launch_norm(const void* x, const void* resid, const void* w, bool w_bf16, f
     go(k_rmsnorm<XT, RT, 512, 1>, 512, 1);
   else if (d <= 8192)
     go(k_rmsnorm<XT, RT, 1024, 1>, 1024, 1);
+  else if (d <= 16384)
+    go(k_rmsnorm<XT, RT, 1024, 2>, 1024, 1);
   else
     go(k_rmsnorm<XT, RT, 1024, 4>, 1024, 1);
 }
@@ -299,10 +320,14 @@ void launch_norm_bwd(const void* du, const void* r, const void* w, bool w_bf16, 
   };
   if (d <= 512)
     go(k_rmsnorm_bwd<GT, RT, 64, 1>, 256);
+  else if (d <= 1024)
+    go(k_rmsnorm_bwd<GT, RT, 64, 2>, 256);
   else if (d <= 2048)
     go(k_rmsnorm_bwd<GT, RT, 256, 1>, 256);
   else if (d <= 8192)
     go(k_rmsnorm_bwd<GT, RT, 256, 4>, 256);
+  else if (d <= 16384)
+    go(k_rmsnorm_bwd<GT, RT, 1024, 2>, 1024);
   else
     go(k_rmsnorm_bwd<GT, RT, 1024, 4>, 1024);
 }
