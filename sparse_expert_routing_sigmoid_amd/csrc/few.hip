@@ -29,12 +29,20 @@
 // and is loaded at device scope, past the caches of one XCD, and each block
 // counts itself after its stores have completed.
 //
+// Measured, d = 7168, I = 2048, 256 routed and one shared expert, K = 8: 4-bit
+// weights and one token 64 us, of them logits 4, selection 9, gate/up 30 (4.2
+// TB/s of weights), down 21 (3.3 TB/s); bf16 and 4 tokens 481 to 490 us (5.7
+// TB/s over the call, gate/up and down 6.3 and 6.0); E4M3 and 32 tokens 1285
+// to 1320 us (5.5 to 5.6 TB/s).  The larger ones are bound by the weight
+// stream, whose ceiling with every CU reading is about 6.1 TB/s; one token of
+// 4-bit weights, 218 MB, by four launches' starts and ends, 3 to 4 us each.
+//
 // Measured against one persistent kernel behind the logits (blocks that take
 // gate/up and then down items from queues, a down item waiting for its
-// expert's gate/up items): 4-bit layer of d = 7168, one token, 75 us against
-// 62; E4M3, 32 tokens, 1433 against 1320.  Its blocks end unevenly (a CU's
-// older waves are served first: 12 us an item against 28 to 49), which the
-// dispatch of fresh blocks evens out.
+// expert's gate/up items), on the products as they then were: 4-bit, one
+// token, 75 us against 69; E4M3, 32 tokens, 1433 against 1343.  Its blocks end
+// unevenly (a CU's older waves are served first: 12 us an item against 28 to
+// 49), which the dispatch of fresh blocks evens out.
 #include "skinny.h"
 #include "vec8.h"
 

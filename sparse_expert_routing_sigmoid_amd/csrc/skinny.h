@@ -115,15 +115,21 @@ struct Skinny {
     for (int f = 0; f < RT; ++f) sc.v[f] = __builtin_amdgcn_raw_buffer_load_b128(L.rs, L.s_off[f], (uint32_t)s * 4u, 0);
   }
 
-  __device__ static __forceinline__ uint32_t past_k(const Lanes& L, int c) {
-    return (c + L.g) * EPL < L.K ? 0u : SK_OOB;
+  __device__ static __forceinline__ uint32_t past_k(const Lanes& L, uint32_t c) {
+    return (int)(c + L.g) * EPL < L.K ? 0u : SK_OOB;
+  }
+  // First chunk of load l of step s as a scalar offset, which has to stay
+  // within the buffer: 0 where the whole load lies past K (its lanes are past
+  // the end by their own offsets).
+  __device__ static __forceinline__ uint32_t base_chunk(const Lanes& L, uint32_t c) {
+    return (int)c * EPL < L.K ? c : 0u;
   }
 
   __device__ static __forceinline__ void load_w(Step& st, const Lanes& L, int s) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
-      const uint32_t c = (uint32_t)(s * LD + l) * 4u;  // first chunk of this load
-      const uint32_t oob = past_k(L, (int)c);
+      const uint32_t first = (uint32_t)(s * LD + l) * 4u, c = base_chunk(L, first);
+      const uint32_t oob = past_k(L, first);
 #pragma unroll
       for (int f = 0; f < RT; ++f)
         st.w[f][l] = __builtin_amdgcn_raw_buffer_load_b128(L.rw, L.w_off[f] | oob, c * 16u, 0);
@@ -142,8 +148,8 @@ struct Skinny {
   __device__ static __forceinline__ void load_x(sk_u32x4 (&x)[NT][LD][XL], const Lanes& L, int s) {
 #pragma unroll
     for (int l = 0; l < LD; ++l) {
-      const uint32_t c = (uint32_t)(s * LD + l) * 4u;
-      const uint32_t oob = past_k(L, (int)c);
+      const uint32_t first = (uint32_t)(s * LD + l) * 4u, c = base_chunk(L, first);
+      const uint32_t oob = past_k(L, first);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t xo = L.x_off[n] | oob;
