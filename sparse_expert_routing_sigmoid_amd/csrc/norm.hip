@@ -291,7 +291,8 @@ template <typename XT, typename RT>
 void launch_norm(const void* x, const void* resid, const void* w, bool w_bf16, float eps, long long T, int d,
                  void* r_out, void* u, bool u_bf16, uint8_t* q, float* q_scale, float* rstd, hipStream_t st) {
   auto go = [&](auto kernel, int threads, int rows) {
-    const long long need = ceil_div(T, rows), most = 1LL << 30;  // further rows in a loop
+    // a launch has fewer than 2^32 threads; further rows in a loop
+    const long long need = ceil_div(T, rows), most = 0xFFFFFFFFLL / threads;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, st,
                        static_cast<const XT*>(x), static_cast<const RT*>(resid), w, w_bf16, eps, T, d,
                        static_cast<RT*>(r_out), u, u_bf16, q, q_scale, rstd);

@@ -213,6 +213,19 @@ def test_past_32_bit_offsets():
     assert bool((x[:2] == 1.0).all()) and bool((x[150_000] == 1.0).all())
 
 
+def test_more_rows_than_one_launch_has_threads_for():
+    T, d = (1 << 26) + 1003, 8                                  # 64 threads to a row: past 2^32 of them
+    x = torch.ones((T, d), dtype=BF16, device="cuda")
+    tail = W.make_free((1100, d), 1.0, 61, "cuda", BF16)
+    x[-1100:] = tail
+    w = torch.ones((d,), device="cuda")
+    u, rstd = torch.zeros_like(x), torch.zeros((T,), device="cuda")
+    M.moe_rmsnorm(x, w, EPS, u=u, rstd=rstd)
+    want = N.rmsnorm(f64_of(tail), None, np.ones(d), EPS)[2]
+    assert np.all(np.abs(f64_of(u[-1100:]) - want) <= out_tol(BF16, np.abs(want), want))
+    assert bool((u[:-1100] == 1.0).all()) and bool((rstd > 0).all())
+
+
 def test_on_another_stream():
     T, d = 64, 1024
     st = torch.cuda.Stream()
