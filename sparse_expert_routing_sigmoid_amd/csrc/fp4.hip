@@ -28,48 +28,55 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
   return c | (__float_as_uint(v) >> 31) << 3;
 }
 
+// Blocks of a launch: fewer than 2^32 threads, further chunks in a loop.
+unsigned chunk_blocks(long long chunks) {
+  const long long need = ceil_div(chunks, 256), most = 0xFFFFFFFFLL / 256;
+  return (unsigned)(need < most ? need : most);
+}
+
 // Eight values per thread; four threads hold a group of 32.  Bound by HBM: 65536
-// x 7168 fp32 values 353 us (6.0 TB/s), bf16 334 us (3.6 TB/s: half the bytes
-// for the same comparisons; weights are quantised once).
+// x 7168 normal fp32 values 429 us (5.0 TB/s), bf16 360 us (3.3 TB/s: half the
+// bytes for the same comparisons; weights are quantised once).
 template <typename XT>
 __global__ __launch_bounds__(256) void k_fp4_quant(const XT* __restrict__ x, long long chunks, uint8_t* __restrict__ q,
                                                    uint8_t* __restrict__ scale) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // chunks % 4 == 0: a group is live or not as one
-  if (i >= chunks) return;
-  float v[8];
-  Vec8<XT>::load(x + i * 8, v);
-  float amax = 0.f;
+  // chunks % 4 == 0: a group is live or not as one
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
+    float v[8];
+    Vec8<XT>::load(x + i * 8, v);
+    float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-  amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
-  amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
-  const int k = e2m1_scale_exp(amax);
-  const float inv = exp2_int(-k);
-  uint32_t w = 0;
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
+    amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
+    const int k = e2m1_scale_exp(amax);
+    const float inv = exp2_int(-k);
+    uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w |= e2m1_code(v[j] * inv) << (4 * j);
-  *reinterpret_cast<uint32_t*>(q + i * 4) = w;
-  if ((i & 3) == 0) scale[i >> 2] = (uint8_t)(k + 127);
+    for (int j = 0; j < 8; ++j) w |= e2m1_code(v[j] * inv) << (4 * j);
+    *reinterpret_cast<uint32_t*>(q + i * 4) = w;
+    if ((i & 3) == 0) scale[i >> 2] = (uint8_t)(k + 127);
+  }
 }
 
-// Bound by HBM: 65536 x 7168 values to bf16 211 us (5.6 TB/s), to fp32 385.
+// Bound by HBM: 65536 x 7168 values to bf16 213 us (5.6 TB/s), to fp32 390.
 template <typename OT>
 __global__ __launch_bounds__(256) void k_fp4_dequant(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                      long long chunks, OT* __restrict__ out) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= chunks) return;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i * 4);
-  const float sc = __uint_as_float((uint32_t)scale[i >> 2] << 23);
-  float v[8];
-  auto put = [&](sk_bf16x2 p, int j) {  // exact: one significant bit beside the leading one
-    v[j] = static_cast<float>(p[0]);
-    v[j + 1] = static_cast<float>(p[1]);
-  };
-  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0), 0);
-  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1), 2);
-  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2), 4);
-  put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3), 6);
-  Vec8<OT>::store(out + i * 8, v);
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(q + i * 4);
+    const float sc = __uint_as_float((uint32_t)scale[i >> 2] << 23);
+    float v[8];
+    auto put = [&](sk_bf16x2 p, int j) {  // exact: one significant bit beside the leading one
+      v[j] = static_cast<float>(p[0]);
+      v[j + 1] = static_cast<float>(p[1]);
+    };
+    put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0), 0);
+    put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1), 2);
+    put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2), 4);
+    put(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 3), 6);
+    Vec8<OT>::store(out + i * 8, v);
+  }
 }
 
 template <typename OT>
@@ -260,7 +267,7 @@ moe_status fp4_quantize(const void* x, moe_dtype x_t, long long rows, long long 
   const long long chunks = rows * (cols / 8);
   if (chunks == 0) return MOE_OK;
   hipStream_t st = as_stream(stream);
-  const dim3 grid((unsigned)ceil_div(chunks, 256));
+  const dim3 grid(chunk_blocks(chunks));
   if (x_t == MOE_F32)
     hipLaunchKernelGGL(k_fp4_quant<float>, grid, dim3(256), 0, st, static_cast<const float*>(x), chunks, q, scale);
   else
@@ -278,7 +285,7 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* scale, long long rows
   const long long chunks = rows * (cols / 8);
   if (chunks == 0) return MOE_OK;
   hipStream_t st = as_stream(stream);
-  const dim3 grid((unsigned)ceil_div(chunks, 256));
+  const dim3 grid(chunk_blocks(chunks));
   if (out_t == MOE_F32)
     hipLaunchKernelGGL(k_fp4_dequant<float>, grid, dim3(256), 0, st, q, scale, chunks, static_cast<float*>(out));
   else

@@ -170,6 +170,27 @@ def test_past_32_bit_offsets():
     assert not y[:, :-40].any()
 
 
+def test_more_values_than_one_launch_has_threads_for():
+    rows, cols = (1 << 21) + 5, 1 << 14                         # 2^35 values and more, eight to a thread
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 110 GiB")
+    tail = W.make_free((6, cols), 1.0, 71, "cuda", BF16)
+    x = torch.ones((rows, cols), dtype=BF16, device="cuda")
+    x[-6:] = tail
+    q = torch.zeros((rows, cols // 2), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((rows, cols // 32), dtype=torch.uint8, device="cuda")
+    M.fp4_quantize_groups(x, q, s)
+    q64, s64 = F.quantize_groups(f64_of(tail))
+    assert np.array_equal(s[-6:].cpu().numpy(), s64) and np.array_equal(q[-6:].cpu().numpy(), q64)
+    assert bool((s[:-6] == int(s[0, 0])).all()) and bool((q[1 << 20] == 0x66).all())   # ones: code 6 (4) at 2^-2
+    x.zero_()
+    M.fp4_dequantize_groups(q, s, x)
+    assert bool((x[:2] == 1.0).all()) and bool((x[1 << 20] == 1.0).all())
+    assert np.array_equal(f64_of(x[-6:]), F.dequantize_groups(q64, s64))
+    del x, q, s
+    torch.cuda.empty_cache()
+
+
 def test_no_rows_and_no_tokens():
     q, s = codes(8, 64, 1)
     M.fp4_matvec(torch.empty((0, 64), dtype=BF16, device="cuda"), q, s, torch.empty((0, 8), device="cuda"))
