@@ -618,7 +618,8 @@ moe_status moe_rmsnorm_backward(const void* du, moe_dtype du_t, const void* r, m
  * fp4_quantize_groups: per group of 32 the smallest 2^k (k >= -126) with
  * amax <= 6 * 2^k (k = 0 for a group of zeros), b = k + 127, and code =
  * round-to-nearest-even(x / 2^k): the rule of fp8_quantize_tiles for this
- * format; finite input never saturates.
+ * format; finite input never saturates.  A group that holds an infinity or a
+ * NaN, which the codes cannot hold, gets b = 255 and codes 0: it reads as NaN.
  *   x, x_t   device [rows, cols], MOE_F32 or MOE_BF16
  *   q        device [rows, cols / 2] uint8 out; scale device [rows, cols / 32]
  *            uint8 out

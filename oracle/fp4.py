@@ -40,13 +40,16 @@ def scale_exp(amax: float) -> int:
 
 
 def quantize_groups(x: np.ndarray):
-    """(q [rows, cols / 2], scale [rows, cols / 32]) uint8 of x [rows, cols]."""
+    """(q [rows, cols / 2], scale [rows, cols / 32]) uint8 of x [rows, cols]; a
+    group with an infinity or a NaN: codes 0 and scale 255 (NaN)."""
     x = np.asarray(x, np.float64)
     rows, cols = x.shape
     grp = x.reshape(rows, cols // GROUP, GROUP)
+    finite = np.isfinite(grp).all(axis=2)
+    grp = np.where(finite[..., None], grp, 0.0)
     k = np.vectorize(scale_exp, otypes=[np.int64])(np.abs(grp).max(axis=2))
     code = encode_rne(grp / np.ldexp(1.0, k)[..., None]).reshape(rows, cols // 2, 2)
-    return (code[..., 0] | code[..., 1] << 4).astype(np.uint8), (k + 127).astype(np.uint8)
+    return (code[..., 0] | code[..., 1] << 4).astype(np.uint8), np.where(finite, k + 127, 255).astype(np.uint8)
 
 
 def dequantize_groups(q: np.ndarray, scale: np.ndarray) -> np.ndarray:

@@ -10,9 +10,8 @@ namespace moe {
 namespace {
 
 // Smallest 2^k (k >= -126) with amax <= 6 * 2^k, or k = 0 for amax == 0: with
-// amax = 1.M * 2^E, k = E - 2 when 1.M <= 1.5, else E - 1.
-__device__ __forceinline__ int e2m1_scale_exp(float amax) {
-  const uint32_t b = __float_as_uint(amax) & 0x7FFFFFFFu;
+// amax = 1.M * 2^E, k = E - 2 when 1.M <= 1.5, else E - 1.  b: bits of amax.
+__device__ __forceinline__ int e2m1_scale_exp(uint32_t b) {
   if (b == 0) return 0;
   const int E = (int)(b >> 23) - 127;
   if (E == -127) return -126;  // subnormal amax
@@ -38,20 +37,22 @@ __global__ __launch_bounds__(256) void k_fp4_quant(const XT* __restrict__ x, lon
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (long long)gridDim.x * 256) {
     float v[8];
     Vec8<XT>::load(x + i * 8, v);
-    float amax = 0.f;
+    // the largest magnitude as an integer: infinities and NaN come out on top
+    uint32_t amax = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
-    amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
-    const int k = e2m1_scale_exp(amax);
+    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
+    const bool finite = amax < 0x7F800000u;
+    const int k = finite ? e2m1_scale_exp(amax) : 0;
     const float sc = exp2_int(k);
     uint32_t w = 0;
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], sc, 0);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], sc, 1);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], sc, 2);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], sc, 3);
-    *reinterpret_cast<uint32_t*>(q + i * 4) = w;
-    if ((i & 3) == 0) scale[i >> 2] = (uint8_t)(k + 127);
+    *reinterpret_cast<uint32_t*>(q + i * 4) = finite ? w : 0u;
+    if ((i & 3) == 0) scale[i >> 2] = finite ? (uint8_t)(k + 127) : 255;
   }
 }
 

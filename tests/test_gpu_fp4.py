@@ -63,6 +63,22 @@ def test_quantize_ties_and_extremes():
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_quantize_infinities_and_nan(dt, bad):
+    x = W.make_free((3, 256), 1.0, 5, "cuda", dt)
+    for r, c in ((0, 0), (1, 77), (2, 255)):
+        x[r, c] = bad
+    q, s = quantized(x)
+    q64, s64 = F.quantize_groups(f64_of(x))
+    assert np.array_equal(s.cpu().numpy(), s64) and np.array_equal(q.cpu().numpy(), q64)
+    back = torch.empty_like(x)
+    M.fp4_dequantize_groups(q, s, back)
+    nan = torch.isnan(back).reshape(3, 8, 32)
+    assert torch.equal(nan.all(dim=2), nan.any(dim=2)) and nan.any(dim=2).sum() == 3
+    assert bool(nan[0, 0].all() and nan[1, 2].all() and nan[2, 7].all())
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 def test_dequantize_every_code_and_scale(dt):
     q = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(256, 1)         # [256, 512 columns]
     s = torch.arange(256, dtype=torch.uint8, device="cuda")[:, None].repeat(1, 16).contiguous()

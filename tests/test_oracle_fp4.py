@@ -41,3 +41,12 @@ def test_round_trip():
     assert np.all(np.abs(v - x) <= np.maximum(0.25 * step, np.abs(x) / 4))
     q2, s2 = F.quantize_groups(v)
     assert np.array_equal(F.dequantize_groups(q2, s2), v)
+
+
+def test_a_group_that_is_not_finite_reads_as_nan():
+    x = np.ones((2, 96))
+    x[0, 40], x[1, 95] = np.inf, np.nan
+    q, s = F.quantize_groups(x)
+    assert s.tolist() == [[125, 255, 125], [125, 125, 255]]
+    nan = np.isnan(F.dequantize_groups(q, s)).reshape(2, 3, 32)
+    assert nan.all(axis=2).tolist() == nan.any(axis=2).tolist() == [[False, True, False], [False, False, True]]
