@@ -644,7 +644,7 @@ moe_status fp4_dequantize_groups(const uint8_t* q, const uint8_t* scale, long lo
  *            when that is 0)
  *   Errors: MOE_EINVAL for NULL pointers, bad sizes (K < 32, K % 32 != 0) or
  *   types; MOE_EUNSUPPORTED for fp32 x, K above 2^20, T above 1048560, N
- *   above 2^34; MOE_EWORKSPACE for a small ws.  T == 0 or N == 0 is valid.
+ *   above 2^27; MOE_EWORKSPACE for a small ws.  T == 0 or N == 0 is valid.
  * ---------------------------------------------------------------------- */
 size_t fp4_matvec_workspace_bytes(int T, long long N, int K);
 moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T,
@@ -678,7 +678,8 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
  *   multiple of 8, K, Nr, Ns as moe_route and moe_permute); MOE_EUNSUPPORTED
  *   for T > MOE_FEW_TOKENS, other type pairs, E4M3 with d or I not a multiple
  *   of 128, E2M1 with d or I not a multiple of 32, an expert's matrix, the
- *   centroids or h of 2 GiB or more; MOE_EWORKSPACE for a small ws.  T == 0 is
+ *   centroids or h of 2 GiB or more, min(T K, Nr) + Ns times I / 16 or d / 32
+ *   of 2^22 or more; MOE_EWORKSPACE for a small ws.  T == 0 is
  *   valid: expert_load is zeroed.
  * ---------------------------------------------------------------------- */
 size_t moe_layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t);

@@ -578,7 +578,8 @@ void launch_blocks(const FewArgs& A, hipStream_t st) {
 
 template <int WT, typename XT>
 void launch_layer(const FewArgs& A, hipStream_t st) {
-  if (WT == MOE_E2M1 && A.d % 128 == 0 && A.I % 128 == 0)
+  // rows of exponent bytes in whole words: read 16 at a time
+  if (WT == MOE_E2M1 && A.d % 128 == 0 && A.I % 128 == 0 && aligned4(A.w13_scale) && aligned4(A.w2_scale))
     launch_blocks<WT, XT, WT == MOE_E2M1>(A, st);
   else
     launch_blocks<WT, XT, false>(A, st);
@@ -634,6 +635,10 @@ moe_status layer_few(const void* u, moe_dtype u_t, const float* centroids, const
                   fits31((unsigned long long)Nr * d * 4) && fits31((unsigned long long)FEW_T * d * 4) &&
                   fits31((unsigned long long)FEW_T * (K + Ns) * I * 4),
               MOE_EUNSUPPORTED, "an expert's matrix, the centroids or h of 2 GiB or more");
+  // blocks of at most 512 threads: a launch has fewer than 2^32
+  const long long experts = (T * K < Nr ? T * K : Nr) + (long long)Ns;
+  MOE_REQUIRE(experts * ceil_div(I, FEW_RT * 8) < (1 << 22) && experts * ceil_div(d, FEW_RT * 16) < (1 << 22),
+              MOE_EUNSUPPORTED, "too many experts for I or d");
   if (T == 0) {
     if (!expert_load) return MOE_OK;
     hipLaunchKernelGGL(k_few_no_load, dim3((Nr + 255) / 256), dim3(256), 0, as_stream(stream), expert_load, Nr);

@@ -300,7 +300,8 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
   MOE_REQUIRE(T >= 0 && N >= 0 && K >= 32 && K % 32 == 0, MOE_EINVAL,
               "need T, N >= 0 and K a positive multiple of 32");
   MOE_REQUIRE(K <= MV_MAX_K, MOE_EUNSUPPORTED, "K above 1048576");
-  MOE_REQUIRE(T <= 16 * 65535 && N <= (1LL << 34), MOE_EUNSUPPORTED, "T above 1048560 or N above 2^34");
+  // 16 threads to a row at most: a launch has fewer than 2^32
+  MOE_REQUIRE(T <= 16 * 65535 && N <= (1LL << 27), MOE_EUNSUPPORTED, "T above 1048560 or N above 2^27");
   if (T == 0 || N == 0) return MOE_OK;
   MOE_REQUIRE(x && q && scale && y, MOE_EINVAL, "NULL pointer");
   MOE_REQUIRE(aligned16(x) && aligned16(q), MOE_EINVAL, "x and q must be 16-byte aligned");
@@ -346,8 +347,10 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     else
       go(k_fp4_matvec<1, 1, SV, true, OT>, MV_W, 16, 4, out);
   };
+  // rows of exponent bytes in whole words: read 16 at a time
+  const bool words = K % 128 == 0 && aligned4(scale);
   auto pick = [&](auto* out) {
-    if (K % 128 == 0) shape(std::true_type{}, out); else shape(std::false_type{}, out);
+    if (words) shape(std::true_type{}, out); else shape(std::false_type{}, out);
   };
   if (y_t == MOE_BF16) pick(static_cast<uint16_t*>(y)); else pick(static_cast<float*>(y));
   return launch_status("fp4_matvec");

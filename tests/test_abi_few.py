@@ -59,6 +59,7 @@ def test_matvec_limits():
     assert matvec(K=(1 << 20) + 32) == M.MOE_EUNSUPPORTED
     assert matvec(T=16 * 65535 + 1) == M.MOE_EUNSUPPORTED
     assert matvec(N=(1 << 34) + 1) == M.MOE_EUNSUPPORTED
+    assert matvec(N=(1 << 27) + 1) == M.MOE_EUNSUPPORTED
     need = M.fp4_matvec_workspace_bytes(3, 40, 64)
     assert need == 0 or matvec(wsb=need - 1) == M.MOE_EWORKSPACE
     assert matvec(T=0, x=None, y=None) == M.MOE_OK and matvec(N=0, y=None) == M.MOE_OK
@@ -82,6 +83,12 @@ def test_few_refuses(kw):
                                 dict(wt=E2M1, I=136), dict(d=1 << 17, I=1 << 13), dict(d=1 << 24)])
 def test_few_does_not_support(kw):
     assert few(**kw) == M.MOE_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(T=32, I=1 << 18, Nr=1024, Ns=0, K=16),
+                                dict(T=32, d=1 << 18, I=128, Nr=1024, Ns=0, K=16)])
+def test_few_refuses_more_blocks_than_a_launch_holds(kw):
+    assert few(wsb=1 << 60, **kw) == M.MOE_EUNSUPPORTED
 
 
 def test_few_workspace():

@@ -115,6 +115,22 @@ def test_fewer_tokens_than_the_layer_holds(n):
         check_out(out, o, f64_of(u[:n]), True)
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_exponent_bytes_at_any_address(off):
+    T, d, Nr, Ns, I, K = 3, 512, 12, 1, 256, 4
+    w, _, _ = weights("e2m1", Nr + Ns, d, I, 17)
+    u, e, b = inputs("e2m1", T, d, Nr, 18)
+    want = M.FewTokenLayer(T, d, Nr, Ns, I, K, BF16, w, out_dtype=F32).forward(u, e, b).clone()
+    for name in ("w13_scale", "w2_scale"):
+        s = getattr(w, name)
+        held = torch.full((s.numel() + 8,), 255, dtype=torch.uint8, device="cuda")
+        held[off:off + s.numel()] = s.flatten()
+        moved = M.ExpertWeights(w.w_t, w.w13, w.w2, w.w13_scale, w.w2_scale)
+        setattr(moved, name, held[off:off + s.numel()].view(s.shape))
+        got = M.FewTokenLayer(T, d, Nr, Ns, I, K, BF16, moved, out_dtype=F32).forward(u, e, b)
+        assert torch.equal(got, want)                           # the same sums in the same order
+
+
 def test_ties_go_to_the_lower_index():
     for Nr in (40, 130, 700):
         d, I, K, T = 64, 32, 6, 5

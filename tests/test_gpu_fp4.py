@@ -174,6 +174,19 @@ def test_nan_scales_of_the_next_row(N, K):
     assert torch.equal(y0[:, keep], y1[:, keep]) and torch.isnan(y1[:, 34]).all() and torch.isnan(y1[:, N - 1]).all()
 
 
+@pytest.mark.parametrize("off", [1, 2, 3, 4])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 1152), (20, 24600, 256), (3, 65600, 128), (17, 65540, 640)])
+def test_exponent_bytes_at_any_address(T, N, K, off):
+    x = W.make_free((T, K), 1.0, 81, "cuda", BF16)
+    q, s = codes(N, K, 82)
+    held = torch.full((s.numel() + 8,), 255, dtype=torch.uint8, device="cuda")
+    at = held[off:off + s.numel()].view(s.shape)
+    at.copy_(s)
+    y = torch.full((T, N), 7.0, device="cuda")
+    M.fp4_matvec(x, q, at, y)
+    check(x, q, s, y)
+
+
 def test_past_32_bit_offsets():
     N, K = 1_250_000, 7168                                      # 4.5e9 bytes of codes
     q = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
