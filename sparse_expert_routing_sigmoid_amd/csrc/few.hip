@@ -15,7 +15,8 @@
 //   k_few_select  one block, a wave per token: scores, selection, gates, the
 //                 list of the touched experts and their tokens.  The blocks
 //                 beside it already run the shared experts' gate/up, which
-//                 needs no selection
+//                 needs no selection.  Small layers do without this launch:
+//                 there each block of k_few_up selects for itself
 //   k_few_up      h = SiLU(W_gate x) (W_up x) of the touched experts, 16
 //                 columns of h of one expert to a block
 //   k_few_down    y = W_down h, fp32, 32 columns of one expert to a block; the
@@ -197,7 +198,7 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
                                                 int t, int lane, int T, int Nr, int K,
                                                 int32_t* topk_idx,
                                                 float* topk_gate, float* topk_score, uint16_t* pick,
-                                                uint32_t* mask) {
+                                                uint32_t* mask, bool write) {
   float s[EPL];
   uint32_t key[EPL];
   uint32_t avail = 0;
@@ -262,11 +263,13 @@ __device__ __forceinline__ void few_route_token(const float* __restrict__ z, int
   }
   if (lane < K) {
     const int o = t * K + lane;
-    topk_idx[o] = my_idx;
     pick[o] = (uint16_t)my_idx;
-    topk_gate[o] = my_s / sum;
-    if (topk_score) topk_score[o] = my_s;
     atomicOr(&mask[my_idx], 1u << t);
+    if (write) {
+      topk_idx[o] = my_idx;
+      topk_gate[o] = my_s / sum;
+      if (topk_score) topk_score[o] = my_s;
+    }
   }
 }
 
@@ -313,22 +316,25 @@ struct FewSelect {
   uint32_t mask[MOE_MAX_EXPERTS];     // tokens of each expert
   uint16_t place[MOE_MAX_EXPERTS];    // its place in the list
   uint16_t pick[FEW_T * MOE_MAX_K];   // [T, K] selected experts
+  int n, wanted;                      // touched experts, and the one at the wanted place of the list
 };
 
-__device__ __forceinline__ void few_select(const FewArgs& A, FewSelect& S, int tid) {
+// Selection by a block of W waves.  write: the outputs and the lists are stored.
+template <int W>
+__device__ __forceinline__ void few_select(const FewArgs& A, FewSelect& S, int tid, bool write, int want) {
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < A.Nr; e += 64 * SELECT_W) S.mask[e] = 0;
+  for (int e = tid; e < A.Nr; e += 64 * W) S.mask[e] = 0;
   __syncthreads();
-  for (int t = wave; t < A.T; t += SELECT_W) {
+  for (int t = wave; t < A.T; t += W) {
     if (A.Nr <= 64)
       few_route_token<1>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
-                         S.mask);
+                         S.mask, write);
     else if (A.Nr <= 256)
       few_route_token<4>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
-                         S.mask);
+                         S.mask, write);
     else
       few_route_token<16>(A.z, A.parts, A.bias, t, lane, A.T, A.Nr, A.K, A.topk_idx, A.topk_gate, A.topk_score, S.pick,
-                          S.mask);
+                          S.mask, write);
   }
   __syncthreads();
   if (wave == 0) {
@@ -340,17 +346,24 @@ __device__ __forceinline__ void few_select(const FewArgs& A, FewSelect& S, int t
       const int at = n + __popcll(b & ((1ull << lane) - 1));
       if (m) {
         S.place[e] = (uint16_t)at;
-        A.lists.expert[at] = e;
-        A.lists.tokens[at] = __popc(m);
+        if (at == want) S.wanted = e;
+        if (write) {
+          A.lists.expert[at] = e;
+          A.lists.tokens[at] = __popc(m);
+        }
       }
       n += __popcll(b);
     }
-    if (lane == 0) *A.lists.n = n;
+    if (lane == 0) {
+      S.n = n;
+      if (write) *A.lists.n = n;
+    }
   }
-  if (A.load)
-    for (int e = tid; e < A.Nr; e += 64 * SELECT_W) A.load[e] = __popc(S.mask[e]);
+  if (write && A.load)
+    for (int e = tid; e < A.Nr; e += 64 * W) A.load[e] = __popc(S.mask[e]);
   __syncthreads();
-  for (int q = tid; q < A.T * A.K; q += 64 * SELECT_W) {
+  if (!write) return;
+  for (int q = tid; q < A.T * A.K; q += 64 * W) {
     const int t = q / A.K, e = S.pick[q];
     A.lists.pair[S.place[e] * FEW_T + __popc(S.mask[e] & ((1u << t) - 1))] = t << 16 | (q - t * A.K);
   }
@@ -505,7 +518,7 @@ __global__ __launch_bounds__(64 * SELECT_W) void k_few_select(FewArgs A) {
   } lds;
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) {
-    few_select(A, lds.select, tid);
+    few_select<SELECT_W>(A, lds.select, tid, true, -1);
     return;
   }
   const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS;
@@ -514,17 +527,48 @@ __global__ __launch_bounds__(64 * SELECT_W) void k_few_select(FewArgs A) {
                              lds.red, tid);
 }
 
-template <int WT, typename XT, bool SV, bool PK>
+// SELF: there was no k_few_select.  Every block of a routed expert selects for
+// itself, the first one stores the results, and the shared experts' blocks
+// come in front.
+template <int WT, typename XT, bool SV, bool PK, bool SELF>
 __global__ __launch_bounds__(FEW_THREADS, PK ? 4 : 1) void k_few_up(FewArgs A) {
-  __shared__ sk_f32x4 red[FEW_W * FEW_RT * 64];
+  __shared__ union {
+    sk_f32x4 red[FEW_W * FEW_RT * 64];
+    FewSelect select;
+  } lds;
+  __shared__ int32_t s_pair[FEW_T];
   const int tid = threadIdx.x;
   const int tiles = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, e = blockIdx.x / tiles;
-  // one memory latency for all four; what lies past the list is not used
-  const int n = *A.lists.n, ex = A.lists.expert[e], toks = A.lists.tokens[e];
-  const int32_t* pairs = A.lists.pair + e * FEW_T;
-  const int p = pairs[tid & 15];
-  if (e >= n) return;
-  few_item<WT, XT, true, SV, PK, FEW_W>(A, ex, toks, pairs, p, (blockIdx.x % tiles) * FEW_UP_COLS, red, tid);
+  int ex, toks, p;
+  const int32_t* pairs;
+  if constexpr (!SELF) {
+    // one memory latency for all four; what lies past the list is not used
+    const int n = *A.lists.n;
+    ex = A.lists.expert[e];
+    toks = A.lists.tokens[e];
+    pairs = A.lists.pair + e * FEW_T;
+    p = pairs[tid & 15];
+    if (e >= n) return;
+  } else if (e < A.Ns) {
+    ex = A.Nr + e;
+    toks = A.T;
+    pairs = nullptr;
+    p = (tid & 15) << 16 | (A.K + e);
+  } else {
+    few_select<FEW_W>(A, lds.select, tid, (int)blockIdx.x == A.Ns * tiles, e - A.Ns);
+    if (e - A.Ns >= lds.select.n) return;
+    ex = __builtin_amdgcn_readfirstlane(lds.select.wanted);
+    const uint32_t m = __builtin_amdgcn_readfirstlane(lds.select.mask[ex]);
+    toks = __popc(m);
+    for (int q = tid; q < A.T * A.K; q += FEW_THREADS) {
+      const int t = q / A.K;
+      if (lds.select.pick[q] == ex) s_pair[__popc(m & ((1u << t) - 1))] = t << 16 | (q - t * A.K);
+    }
+    __syncthreads();  // red lies on the selection
+    pairs = s_pair;
+    p = pairs[tid & 15];
+  }
+  few_item<WT, XT, true, SV, PK, FEW_W>(A, ex, toks, pairs, p, (blockIdx.x % tiles) * FEW_UP_COLS, lds.red, tid);
 }
 
 template <int WT, typename XT, bool SV, bool PK>
@@ -548,6 +592,18 @@ __global__ __launch_bounds__(FEW_THREADS, PK ? 4 : 1) void k_few_down(FewArgs A)
     few_combine(A, tile * FEW_DOWN_COLS, tid);
 }
 
+// Whether the gate/up blocks select for themselves, which saves a launch and
+// costs every block the selection of T / FEW_W tokens by each wave, in length
+// about as the experts of a lane.  In us, with k_few_select and without: fp32, d
+// = 256, 16 + 1 experts, one token 18.2 / 15.6, 8 tokens 19.3 / 16.6, 32 23.3 /
+// 25.7; bf16, d = 2048, I = 1408, 64 + 2 experts, one token 44 / 39, 2 65 / 61,
+// 4 90 / 88, 8 126 / 132; 4-bit, d = 7168, 256 + 1 experts, one token, I = 512
+// 33.0 / 31.6, I = 2048 64.7 / 67.7, with 64 + 1 experts 64.4 / 63.3.
+bool few_selects_for_itself(const FewArgs& A, int blocks) {
+  const int lane = A.Nr <= 64 ? 1 : A.Nr <= 256 ? 4 : 16, tokens = (A.T + FEW_W - 1) / FEW_W;
+  return A.T <= 2 * FEW_W && blocks * tokens * lane <= 2560;
+}
+
 // Packed where an expert has few tokens: at most two for every routed expert
 // on average, or no more tokens than fit.  (d = 7168, 256 experts, whole
 // layer: E4M3, 32 tokens, 1285 us against 1330; 4-bit, one token, 66 against
@@ -562,18 +618,24 @@ void launch_blocks(const FewArgs& A, hipStream_t st) {
   const int up = (A.I + FEW_UP_COLS - 1) / FEW_UP_COLS, down = (A.d + FEW_DOWN_COLS - 1) / FEW_DOWN_COLS;
   const dim3 block(FEW_THREADS);
   auto select = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(1 + A.Ns * up), dim3(64 * SELECT_W), 0, st, A); };
-  auto products = [&](auto k_up, auto k_down) {
-    hipLaunchKernelGGL(k_up, dim3(touched * up), block, 0, st, A);
+  const bool self = few_selects_for_itself(A, (touched + A.Ns) * up);
+  auto products = [&](auto k_up, auto k_self, auto k_down) {
+    if (self)
+      hipLaunchKernelGGL(k_self, dim3((touched + A.Ns) * up), block, 0, st, A);
+    else
+      hipLaunchKernelGGL(k_up, dim3(touched * up), block, 0, st, A);
     hipLaunchKernelGGL(k_down, dim3((touched + A.Ns) * down), block, 0, st, A);
   };
-  if (NARROW && A.T <= PACKED)
-    select(k_few_select<WT, XT, SV, NARROW>);
-  else
-    select(k_few_select<WT, XT, SV, false>);
+  if (!self) {
+    if (NARROW && A.T <= PACKED)
+      select(k_few_select<WT, XT, SV, NARROW>);
+    else
+      select(k_few_select<WT, XT, SV, false>);
+  }
   if (NARROW && (A.T <= PACKED || A.T * A.K <= 2 * A.Nr))
-    products(k_few_up<WT, XT, SV, NARROW>, k_few_down<WT, XT, SV, NARROW>);
+    products(k_few_up<WT, XT, SV, NARROW, false>, k_few_up<WT, XT, SV, NARROW, true>, k_few_down<WT, XT, SV, NARROW>);
   else
-    products(k_few_up<WT, XT, SV, false>, k_few_down<WT, XT, SV, false>);
+    products(k_few_up<WT, XT, SV, false, false>, k_few_up<WT, XT, SV, false, true>, k_few_down<WT, XT, SV, false>);
 }
 
 template <int WT, typename XT>

@@ -60,7 +60,9 @@ CASES = [("f32", 1, 256, 16, 1, 128, 4), ("f32", 7, 264, 20, 2, 136, 3), ("f32",
          ("bf16", 32, 520, 300, 1, 72, 8), ("bf16", 3, 2048, 64, 2, 1408, 6), ("bf16", 4, 64, 1023, 1, 32, 16),
          ("bf16", 2, 8, 1, 0, 8, 1), ("e4m3", 1, 256, 16, 1, 128, 4), ("e4m3", 19, 384, 40, 1, 256, 8),
          ("e4m3", 32, 128, 8, 3, 128, 8), ("e2m1", 1, 256, 16, 1, 128, 4), ("e2m1", 5, 288, 24, 1, 160, 4),
-         ("e2m1", 32, 96, 8, 2, 32, 8), ("e2m1", 20, 1024, 257, 0, 64, 7), ("e2m1", 2, 32, 3, 1, 32, 1)]
+         ("e2m1", 32, 96, 8, 2, 32, 8), ("e2m1", 20, 1024, 257, 0, 64, 7), ("e2m1", 2, 32, 3, 1, 32, 1),
+         ("e4m3", 6, 256, 12, 2, 128, 5), ("bf16", 8, 512, 64, 1, 256, 6), ("bf16", 2, 64, 300, 1, 2080, 16),
+         ("e2m1", 8, 128, 200, 1, 64, 8)]
 
 
 @pytest.mark.parametrize("wt,T,d,Nr,Ns,I,K", CASES)
