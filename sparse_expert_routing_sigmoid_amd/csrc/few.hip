@@ -412,7 +412,7 @@ __device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, 
                                    (PK ? (uint32_t)(lane % S::XV) * 16u : 0u)
                              : SK_OOB;
   sk_f32x4 acc[RT][S::AC];
-  S::template run_part<FEW_D>(acc, L, 0, (Kd + S::STEP - 1) / S::STEP, wave, W);
+  S::template run_part<FEW_D, WT == MOE_E2M1 ? 2 : 1>(acc, L, 0, (Kd + S::STEP - 1) / S::STEP, wave, W);
   if constexpr (PK)
     sk_put_packed<RT, S::XV>(red, acc, tid);
   else

@@ -148,18 +148,19 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
 // more than the weights: 65536 x 7168 rows and 16 tokens took 150, 101, 77
 // and 68 us with 1, 2, 4 and 8 row tiles to a wave.)  In LDS a fragment is 64
 // consecutive 16-byte words, the lanes' own, so its reads have no bank
-// conflicts.  65536 x 7168 and 16 tokens 62 us, 4.1 TB/s of weights (54 us with
-// one token): one or two blocks a CU and a barrier a chunk keep it from the 6.1
-// TB/s that a plain stream reaches.
+// conflicts.  A step takes half a cache line of each row, so two steps' loads
+// are issued together: apart, the line was fetched twice (65536 x 7168, 16
+// tokens, 62 us; two steps ahead, apart, 58; now 55, 4.6 TB/s of weights; 49
+// with one token).  What a CU takes in at a time bounds it, 19 KB a
+// microsecond: two blocks on one run at half the speed each.
 constexpr int ML_W = 8;   // waves
-constexpr int ML_D = 4;   // steps the weights' loads run ahead
 
 template <int RT, int NT, bool SV, typename OT>
 __global__ __launch_bounds__(64 * ML_W) void k_fp4_matvec_lds(const uint16_t* __restrict__ x,
                                                               const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ scale, int T, long long N,
                                                               int K, OT* __restrict__ y) {
-  constexpr int D = ML_D, CH = 8 / NT;
+  constexpr int D = RT == 1 ? 4 : 2, G = 2, CH = 8 / NT;  // steps the weights' loads run ahead, and come together
   using S = Skinny<MOE_E2M1, uint16_t, RT, NT, SV>;
   constexpr int FRAGS = CH * NT * S::XV, MINE = FRAGS / ML_W;  // fragments of a chunk, and those that a wave stages
   static_assert(FRAGS % ML_W == 0 && CH % D == 0, "chunks are staged by all waves, and are turns of the ring");
@@ -234,7 +235,9 @@ __global__ __launch_bounds__(64 * ML_W) void k_fp4_matvec_lds(const uint16_t* __
         S::mma(acc, st[i % D], L, sc[0], i % 4);
       }
       __builtin_amdgcn_sched_barrier(0);
-      S::load_w(st[i % D], L, s + D);
+      if (i % G == G - 1)
+#pragma unroll
+        for (int j = i - G + 1; j <= i; ++j) S::load_w(st[j % D], L, c * CH + j + D);
       __builtin_amdgcn_sched_barrier(0);
       if (SV && i % 4 == 3) sc[0] = sc[1];
     }
@@ -314,22 +317,30 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     const dim3 grid((unsigned)ceil_div(N, rows), (unsigned)ceil_div(T, tokens));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, xb, q, scale, T, N, K, out);
   };
-  // At K = 7168, in us.  Up to 4 tokens, packed, 1 and 4 tokens: 4096 rows 6.0
-  // / 6.1 with one row tile to a block, 7.8 / 7.9 with two (not packed 6.6 /
-  // 7.6); 16384: 12.8 / 13.3, two 13.4 / 13.4; 32768: 31 / 35, two 28 / 31;
-  // 65536: 54 / 67, two 56 / 57, through LDS 54 / 56.
-  // More tokens, 16 and 32: 4096 rows, one tile 11 / 17, two 13 / 19; 8192: two
-  // 13 / 19, one 18 / 30, four 17 / 23; 16384: four 18 / 25, two 22 / 37,
-  // through LDS 23 / 32; 32768: LDS 34 / 43, four 40 / 55; 65536: LDS, two tiles
-  // to a wave 62 / 72, one 66 / 82, without LDS 81 / 108.
+  // In us, K = 7168.  Through LDS a CU takes 128 rows at a time in about 27 (up
+  // to 16 tokens; 32 tokens 34) and 256 in twice that, however many of its
+  // neighbours have none left: `units` of 32768 rows, with one row tile to a wave
+  // when their number is odd (81920 rows, 16 tokens, 86, with two tiles 105), else
+  // two (65536: 55 / 60; 131072: 118 / 120).  The other form takes 40 a unit (32
+  // tokens 55), up to 4 tokens packed 27 to 31, of the rows there are: LDS where
+  // enough of the last unit is filled (32768 rows, one token 28 / 30, 4 tokens 29 /
+  // 33, 16 tokens 33 / 40; 65536: 49 / 53, 52 / 62, 55 / 81; 100003, 2 tokens:
+  // 95 / 87).
+  // Below that, rows to a block, up to 4 tokens, packed, 1 and 4 tokens: 4096
+  // rows 6.0 / 6.1 with one row tile, 7.8 / 7.9 with two (not packed 6.6 / 7.6);
+  // 16384: 12.8 / 13.3, two 13.4 / 13.4; 32768: 31 / 35, two 28 / 31.  16 and 32
+  // tokens: 4096 rows, one tile 11 / 17, two 13 / 19; 8192: two 13 / 19, one 18 /
+  // 30, four 17 / 23; 16384: four 18 / 25, two 22 / 37, LDS 23 / 32.
+  const long long units = ceil_div(N, 32768);
+  const bool lds = N * 16 >= units * 32768 * (T > 4 ? 11 : 14);
   auto shape = [&](auto sv, auto* out) {
     constexpr bool SV = decltype(sv)::value;
     using OT = std::remove_pointer_t<decltype(out)>;
     auto many = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      if (N >= 65536)
+      if (lds && units % 2 == 0)
         go(k_fp4_matvec_lds<2, NT, SV, OT>, ML_W, 32 * ML_W, 16 * NT, out);
-      else if (N >= 24576)
+      else if (lds)
         go(k_fp4_matvec_lds<1, NT, SV, OT>, ML_W, 16 * ML_W, 16 * NT, out);
       else if (N >= 12288)
         go(k_fp4_matvec<4, NT, SV, false, OT>, MV_W, 64, 16 * NT, out);
@@ -340,7 +351,7 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     };
     if (T > 16)
       many(std::integral_constant<int, 2>{});
-    else if (T > 4)
+    else if (T > 4 || lds)
       many(std::integral_constant<int, 1>{});
     else if (N >= 24576)
       go(k_fp4_matvec<2, 1, SV, true, OT>, MV_W, 32, 4, out);

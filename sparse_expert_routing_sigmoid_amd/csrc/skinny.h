@@ -227,13 +227,14 @@ struct Skinny {
     }
   }
 
-  // Steps s0 to s1 - 1, loads D steps ahead.  The branches are uniform: no
-  // step past the end is loaded or multiplied (a wave has few steps, so
-  // rounding their number up to D costs more than the branches).
-  template <int D>
+  // Steps s0 to s1 - 1, loads D steps ahead, those of G steps together.  The
+  // branches are uniform: no step past the end is loaded or multiplied (a wave
+  // has few steps, so rounding their number up to D costs more than the
+  // branches).
+  template <int D, int G = 1>
   __device__ static __forceinline__ void run(sk_f32x4 (&acc)[RT][AC], const Lanes& L, int s0, int s1) {
     constexpr int U = SV ? 4 : D;  // steps to a turn of the loop: a vector holds the exponent bytes of four
-    static_assert(U % D == 0, "a turn of the loop goes round the ring");
+    static_assert(U % D == 0 && D % G == 0, "a turn of the loop goes round the ring");
 #pragma unroll
     for (int f = 0; f < RT; ++f)
 #pragma unroll
@@ -255,7 +256,9 @@ struct Skinny {
       for (int i = 0; i < U; ++i) {
         mma(acc, st[i % D], L, sc[0], i);
         __builtin_amdgcn_sched_barrier(0);
-        load(st[i % D], L, s + D + i);
+        if (i % G == G - 1)
+#pragma unroll
+          for (int j = i - G + 1; j <= i; ++j) load(st[j % D], L, s + D + j);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (SV) sc[0] = sc[1];
@@ -265,16 +268,19 @@ struct Skinny {
     for (int i = 0; i < U + D - 1; ++i) {
       if (s + i < s1) mma(acc, st[i % D], L, sc[i / U], i % U);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < U - 1 && s + D + i < s1) load(st[i % D], L, s + D + i);
+      if (i < U && i % G == G - 1)
+#pragma unroll
+        for (int j = i - G + 1; j <= i; ++j)
+          if (s + D + j < s1) load(st[j % D], L, s + D + j);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // Wave w of W: steps [s0, s1) cut into W runs of equal length (or one less).
-  template <int D>
+  template <int D, int G = 1>
   __device__ static __forceinline__ void run_part(sk_f32x4 (&acc)[RT][AC], const Lanes& L, int s0, int s1, int w, int W) {
     const int n = s1 > s0 ? s1 - s0 : 0;
-    run<D>(acc, L, s0 + n * w / W, s0 + n * (w + 1) / W);
+    run<D, G>(acc, L, s0 + n * w / W, s0 + n * (w + 1) / W);
   }
 };
 

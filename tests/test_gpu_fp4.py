@@ -120,7 +120,7 @@ def test_matvec(T, N, K, yt):
 
 @pytest.mark.parametrize("T", [1, 16, 31])
 @pytest.mark.parametrize("N,K", [(8200, 384), (16390, 288), (16390, 640), (24580, 1152), (30001, 1056), (65540, 288),
-                                 (65537, 2176)])
+                                 (65537, 2176), (45060, 288), (45060, 1152), (65530, 2176), (29000, 640)])
 def test_matvec_many_rows(T, N, K):
     x = W.make_free((T, K), 1.0, T, "cuda", BF16)
     q, s = codes(N, K, T)
@@ -159,7 +159,7 @@ def test_nan_stays_in_its_row_and_token():
     assert torch.isnan(y1[4]).all() and torch.isnan(y1[:, 33]).all() and not torch.isfinite(y1[17]).any()
 
 
-@pytest.mark.parametrize("N", [100, 24576, 65600])
+@pytest.mark.parametrize("N", [100, 24576, 65600, 65500])
 @pytest.mark.parametrize("K", [1152, 1056, 128])
 def test_nan_scales_of_the_next_row(N, K):
     """A row whose first groups are NaN, behind a row that ends inside a block's turn of K."""
@@ -175,7 +175,8 @@ def test_nan_scales_of_the_next_row(N, K):
 
 
 @pytest.mark.parametrize("off", [1, 2, 3, 4])
-@pytest.mark.parametrize("T,N,K", [(1, 40, 1152), (20, 24600, 256), (3, 65600, 128), (17, 65540, 640)])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 1152), (20, 24600, 256), (3, 65600, 128), (17, 65540, 640),
+                                   (2, 65530, 640)])
 def test_exponent_bytes_at_any_address(T, N, K, off):
     x = W.make_free((T, K), 1.0, 81, "cuda", BF16)
     q, s = codes(N, K, 82)
