@@ -31,10 +31,10 @@
 // counts itself after its stores have completed.
 //
 // Measured, d = 7168, I = 2048, 256 routed and one shared expert, K = 8: 4-bit
-// weights and one token 64 us, of them logits 4, selection 9, gate/up 30 (4.2
-// TB/s of weights), down 21 (3.3 TB/s); bf16 and 4 tokens 481 to 490 us (5.7
-// TB/s over the call, gate/up and down 6.3 and 6.0); E4M3 and 32 tokens 1285
-// to 1320 us (5.5 to 5.6 TB/s).  The larger ones are bound by the weight
+// weights and one token 64 us, of them logits 5, selection 8, gate/up 24 (5.2
+// TB/s of weights), down 19 (3.7 TB/s); bf16 and 4 tokens 481 to 490 us (5.7
+// TB/s over the call, gate/up and down 6.3 and 6.0); E4M3 and 32 tokens 1264
+// to 1330 us (5.4 to 5.7 TB/s).  The larger ones are bound by the weight
 // stream, whose ceiling with every CU reading is about 6.1 TB/s; one token of
 // 4-bit weights, 218 MB, by four launches' starts and ends, 3 to 4 us each.
 //

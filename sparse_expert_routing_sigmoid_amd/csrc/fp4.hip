@@ -150,9 +150,9 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
 // consecutive 16-byte words, the lanes' own, so its reads have no bank
 // conflicts.  A step takes half a cache line of each row, so two steps' loads
 // are issued together: apart, the line was fetched twice (65536 x 7168, 16
-// tokens, 62 us; two steps ahead, apart, 58; now 55, 4.6 TB/s of weights; 49
-// with one token).  What a CU takes in at a time bounds it, 19 KB a
-// microsecond: two blocks on one run at half the speed each.
+// tokens, 62 us; two steps ahead, apart, 58; now 55, of them 48 in the kernel,
+// 5.2 TB/s; 49 with one token).  What a CU takes in at a time bounds it, 20 KB
+// a microsecond: two blocks on one run at half the speed each.
 constexpr int ML_W = 8;   // waves
 
 template <int RT, int NT, bool SV, typename OT>
