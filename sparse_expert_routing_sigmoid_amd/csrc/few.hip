@@ -431,7 +431,7 @@ __device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, 
   constexpr int OUT_TILES = UP ? RT / 2 : RT;
   for (int i = tid; i < OUT_TILES * 64; i += 64 * W) {
     const int f = i >> 6, c = col0 + f * 16 + 4 * L.g;  // 64 threads to a tile: each its own lane's column
-    if (j0 + (lane & 15) >= toks || c >= Nd) continue;  // Nd % 4 == 0: four columns exist or none
+    if (!S::holds(lane, j0, toks) || c >= Nd) continue;  // Nd % 4 == 0: four columns exist or none
     const long long o = (long long)hr * Nd + c;
     const sk_f32x4 a = sum(f);
     if constexpr (UP) {

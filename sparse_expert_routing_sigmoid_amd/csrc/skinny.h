@@ -91,6 +91,13 @@ struct Skinny {
   static_assert(!PK || NT == 1, "one tile of columns");
   static_assert(WT == MOE_F32 || sizeof(XT) == 2, "narrow weights take bf16 tokens");
 
+  // Whether a tile of tokens j0 .. j0 + TOKENS - 1 of `toks` holds the sums of
+  // column lane % 16: a packed tile holds fewer tokens than it has columns, and
+  // what sk_get_packed finds for the others is another row group's or no one's.
+  __host__ __device__ static constexpr bool holds(int lane, int j0, int toks) {
+    return (lane & 15) < TOKENS && j0 + (lane & 15) < toks;
+  }
+
   struct Lanes {
     __amdgpu_buffer_rsrc_t rw, rs, rx;
     uint32_t w_off[RT];  // byte offset of the lane's row of tile f, chunk l / 16 included; SK_OOB: no such row
@@ -320,9 +327,14 @@ __device__ __forceinline__ void sk_put_packed(sk_f32x4* red, const sk_f32x4 (&ac
   }
   __syncthreads();
 }
+// Its first column of the 64 values of a wave's row tile.
+template <int XV>
+__host__ __device__ constexpr int sk_packed_at(int lane) {
+  return (lane & 48) + (lane & 15) * XV;
+}
 template <int W, int RT, int XV>
 __device__ __forceinline__ sk_f32x4 sk_get_packed(const sk_f32x4* red, int f, int lane) {
-  const int at = (lane & 48) + (lane & 15) * XV;
+  const int at = sk_packed_at<XV>(lane);
   sk_f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < W; ++w) {
