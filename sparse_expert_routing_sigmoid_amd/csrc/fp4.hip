@@ -201,9 +201,9 @@ __global__ __launch_bounds__(64 * ML_W) void k_fp4_matvec_lds(const uint16_t* __
   auto put = [&](int c) {
 #pragma unroll
     for (int m = 0; m < MINE; ++m) lds[c & 1][wave * MINE + m][lane] = stage[m];
-    // the LDS writes alone are waited for: the loads in flight stay so
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+    // the LDS writes alone are waited for: the loads in flight stay so.  One
+    // statement, so that no access comes to lie between the wait and the barrier
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
   sk_f32x4 acc[RT][NT];
 #pragma unroll
