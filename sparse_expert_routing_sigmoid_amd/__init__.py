@@ -447,17 +447,56 @@ def moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t):
     return lib().moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t)
 
 
+def _rows(t, T, K, dtype, name):
+    """t is [at least T, K]: the call writes its first T rows."""
+    if t is not None and (t.dim() != 2 or t.shape[0] < T or t.shape[1] != K or t.dtype != dtype):
+        raise ValueError(f"{name}: expected at least {(T, K)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _few_weights(w: "ExpertWeights", E, d, I):
+    """w holds E experts of width I in one of moe_layer_few's weight types."""
+    store = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_E4M3: torch.uint8, MOE_E2M1: torch.uint8}
+    if w.w_t not in store:
+        raise ValueError(f"w_t: unknown weight type {w.w_t}")
+    per_byte = 2 if w.w_t == MOE_E2M1 else 1
+    _shape(w.w13, (E, 2 * I, d // per_byte), store[w.w_t], "w13")
+    _shape(w.w2, (E, d, I // per_byte), store[w.w_t], "w2")
+    if w.w_t in (MOE_E4M3, MOE_E2M1) and (w.w13_scale is None or w.w2_scale is None):
+        raise ValueError("E4M3 and E2M1 weights need scales")
+    if w.w_t == MOE_E4M3:
+        _shape(w.w13_scale, (E, 2 * I // 128, d // 128), torch.float32, "w13_scale")
+        _shape(w.w2_scale, (E, d // 128, I // 128), torch.float32, "w2_scale")
+    if w.w_t == MOE_E2M1:
+        _shape(w.w13_scale, (E, 2 * I, d // 32), torch.uint8, "w13_scale")
+        _shape(w.w2_scale, (E, d, I // 32), torch.uint8, "w2_scale")
+
+
 def moe_layer_few(u, centroids, bias, w: "ExpertWeights", Ns, I, K, resid, topk_idx, topk_gate, topk_score, expert_load,
                   ws, out, stream=None):
     """The whole layer for up to MOE_FEW_TOKENS tokens u [T, d]; resid [T, d]
-    or None is added to out [T, d]."""
+    or None is added to out [T, d].  The first T rows of topk_idx, topk_gate
+    and topk_score (or None) are written."""
     T, d = u.shape
     Nr = centroids.shape[0]
+    _few_weights(w, Nr + Ns, d, I)
+    _shape(centroids, (Nr, d), torch.float32, "centroids")
+    _shape(bias, (Nr,), torch.float32, "bias")
+    _same(resid, u, "resid")
+    _rows(topk_idx, T, K, torch.int32, "topk_idx")
+    _rows(topk_gate, T, K, torch.float32, "topk_gate")
+    _rows(topk_score, T, K, torch.float32, "topk_score")
+    _shape(expert_load, (Nr,), torch.int32, "expert_load")
+    _same(out, u, "out")
+    _layer_few(u, centroids, bias, w, Ns, I, K, resid, topk_idx, topk_gate, topk_score, expert_load, ws, out, stream)
+
+
+def _layer_few(u, centroids, bias, w, Ns, I, K, resid, topk_idx, topk_gate, topk_score, expert_load, ws, out, stream):
+    T, d = u.shape
     _check(lib().moe_layer_few(_ptr(u), dtype_code(u), _ptr(centroids), _ptr(bias), w.w_t, _ptr(w.w13),
-                               _ptr(w.w13_scale), _ptr(w.w2), _ptr(w.w2_scale), T, d, Nr, Ns, I, K, _ptr(resid),
-                               MOE_F32 if resid is None else dtype_code(resid), _ptr(topk_idx), _ptr(topk_gate),
-                               _ptr(topk_score), _ptr(expert_load), _ptr(ws), _nbytes(ws), _ptr(out), dtype_code(out),
-                               _stream(stream)))
+                               _ptr(w.w13_scale), _ptr(w.w2), _ptr(w.w2_scale), T, d, centroids.shape[0], Ns, I, K,
+                               _ptr(resid), MOE_F32 if resid is None else dtype_code(resid), _ptr(topk_idx),
+                               _ptr(topk_gate), _ptr(topk_score), _ptr(expert_load), _ptr(ws), _nbytes(ws), _ptr(out),
+                               dtype_code(out), _stream(stream)))
 
 
 # ------------------------------------------------------- layer plumbing --
@@ -514,20 +553,7 @@ class FewTokenLayer:
         self.act_dtype, self.w = act_dtype, weights
         if not 0 <= T <= MOE_FEW_TOKENS:
             raise ValueError(f"T: at most {MOE_FEW_TOKENS} tokens")
-        E = Nr + Ns
-        per_byte = 2 if weights.w_t == MOE_E2M1 else 1
-        store = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_E4M3: torch.uint8,
-                 MOE_E2M1: torch.uint8}[weights.w_t]
-        _shape(weights.w13, (E, 2 * I, d // per_byte), store, "w13")
-        _shape(weights.w2, (E, d, I // per_byte), store, "w2")
-        if weights.w_t in (MOE_E4M3, MOE_E2M1) and (weights.w13_scale is None or weights.w2_scale is None):
-            raise ValueError("E4M3 and E2M1 weights need scales")
-        if weights.w_t == MOE_E4M3:
-            _shape(weights.w13_scale, (E, 2 * I // 128, d // 128), torch.float32, "w13_scale")
-            _shape(weights.w2_scale, (E, d // 128, I // 128), torch.float32, "w2_scale")
-        if weights.w_t == MOE_E2M1:
-            _shape(weights.w13_scale, (E, 2 * I, d // 32), torch.uint8, "w13_scale")
-            _shape(weights.w2_scale, (E, d, I // 32), torch.uint8, "w2_scale")
+        _few_weights(weights, Nr + Ns, d, I)
         dev = torch.device(device)
         self.topk_idx = torch.empty((T, K), dtype=torch.int32, device=dev)
         self.topk_gate = torch.empty((T, K), dtype=torch.float32, device=dev)
@@ -552,8 +578,8 @@ class FewTokenLayer:
         _shape(bias, (self.Nr,), torch.float32, "bias")
         resid = None if flags else u if residual is None else residual
         out = self.out if n == self.T else self.out[:n]
-        moe_layer_few(u, centroids, bias, self.w, self.Ns, self.I, self.K, resid, self.topk_idx, self.topk_gate,
-                      self.topk_score, self.expert_load, self.ws, out, stream)
+        _layer_few(u, centroids, bias, self.w, self.Ns, self.I, self.K, resid, self.topk_idx, self.topk_gate,
+                   self.topk_score, self.expert_load, self.ws, out, stream)
         return out
 
     def update_bias(self, bias, tokens=None, gamma=0.001, stream=None):
