@@ -563,6 +563,7 @@ class FewTokenLayer:
         u_t = MOE_BF16 if act_dtype == torch.bfloat16 else MOE_F32
         self.ws = torch.empty((max(moe_layer_few_workspace_bytes(T, d, Nr, Ns, I, K, u_t), 1),), dtype=torch.uint8,
                               device=dev)
+        self.tokens = T  # of the last forward()
 
     def forward(self, u, centroids, bias, residual=None, flags=0, stream=None):
         """out [n, d] = residual + the experts' part for u [n, d], n <= T.
@@ -580,11 +581,14 @@ class FewTokenLayer:
         out = self.out if n == self.T else self.out[:n]
         _layer_few(u, centroids, bias, self.w, self.Ns, self.I, self.K, resid, self.topk_idx, self.topk_gate,
                    self.topk_score, self.expert_load, self.ws, out, stream)
+        self.tokens = n
         return out
 
     def update_bias(self, bias, tokens=None, gamma=0.001, stream=None):
-        """End-of-step bias rule for the loads of the last forward() of `tokens` tokens (T by default)."""
-        moe_bias_update(self.expert_load, (self.T if tokens is None else tokens) * self.K, gamma, bias, stream)
+        """End-of-step bias rule for the loads of the last call: by default
+        forward()'s, of as many tokens as it had (the replay of a captured
+        call is none: give its `tokens` where they may differ)."""
+        moe_bias_update(self.expert_load, (self.tokens if tokens is None else tokens) * self.K, gamma, bias, stream)
 
 
 class MoeLayer:
