@@ -642,11 +642,11 @@ moe_status fp4_dequantize_groups(const uint8_t* q, const uint8_t* scale, long lo
  *   x, x_t   device [T, K], MOE_BF16
  *   q, scale device [N, K / 2], [N, K / 32] uint8
  *   y, y_t   device [T, N] out, MOE_F32 or MOE_BF16 (element alignment)
- *   ws       device, fp4_matvec_workspace_bytes(T, N, K) bytes (may be NULL
- *            when that is 0)
+ *   ws       not used, may be NULL: fp4_matvec_workspace_bytes(T, N, K) is 0
+ *            for all sizes
  *   Errors: MOE_EINVAL for NULL pointers, bad sizes (K < 32, K % 32 != 0) or
  *   types; MOE_EUNSUPPORTED for fp32 x, K above 2^20, T above 1048560, N
- *   above 2^27; MOE_EWORKSPACE for a small ws.  T == 0 or N == 0 is valid.
+ *   above 2^27.  T == 0 or N == 0 is valid.
  * ---------------------------------------------------------------------- */
 size_t fp4_matvec_workspace_bytes(int T, long long N, int K);
 moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T,

@@ -97,9 +97,8 @@ moe_status fp4_quantize(const void* x, moe_dtype x_t, long long rows, long long 
                         void* stream);
 moe_status fp4_dequantize(const uint8_t* q, const uint8_t* scale, long long rows, long long cols, void* out,
                           moe_dtype out_t, void* stream);
-size_t fp4_matvec_workspace_bytes(int T, long long N, int K);
 moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
-                      void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream);
+                      void* y, moe_dtype y_t, void* stream);
 size_t layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t);
 moe_status layer_few(const void* u, moe_dtype u_t, const float* centroids, const float* bias, moe_dtype w_t,
                      const void* w13, const void* w13_scale, const void* w2, const void* w2_scale, int T, int d, int Nr,
@@ -368,12 +367,13 @@ moe_status fp4_dequantize_groups(const uint8_t* q, const uint8_t* scale, long lo
   return moe::fp4_dequantize(q, scale, rows, cols, out, out_t, stream);
 }
 
-size_t fp4_matvec_workspace_bytes(int T, long long N, int K) { return moe::fp4_matvec_workspace_bytes(T, N, K); }
+// no form of the product shares anything between blocks
+size_t fp4_matvec_workspace_bytes(int T, long long N, int K) { return 0; }
 
 moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
                       void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream) {
   moe::clear_error();
-  return moe::fp4_matvec(x, x_t, q, scale, T, N, K, y, y_t, ws, ws_bytes, stream);
+  return moe::fp4_matvec(x, x_t, q, scale, T, N, K, y, y_t, stream);
 }
 
 size_t moe_layer_few_workspace_bytes(int T, int d, int Nr, int Ns, int I, int K, moe_dtype u_t) {

@@ -293,10 +293,8 @@ moe_status fp4_dequantize(const uint8_t* q, const uint8_t* scale, long long rows
   return launch_status("fp4_dequantize_groups");
 }
 
-size_t fp4_matvec_workspace_bytes(int T, long long N, int K) { return 0; }
-
 moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint8_t* scale, int T, long long N, int K,
-                      void* y, moe_dtype y_t, void* ws, size_t ws_bytes, void* stream) {
+                      void* y, moe_dtype y_t, void* stream) {
   MOE_REQUIRE(x_t == MOE_F32 || x_t == MOE_BF16, MOE_EINVAL, "x_t must be MOE_F32 or MOE_BF16");
   MOE_REQUIRE(y_t == MOE_F32 || y_t == MOE_BF16, MOE_EINVAL, "y_t must be MOE_F32 or MOE_BF16");
   MOE_REQUIRE(x_t == MOE_BF16, MOE_EUNSUPPORTED, "x must be bf16");
@@ -308,8 +306,6 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
   if (T == 0 || N == 0) return MOE_OK;
   MOE_REQUIRE(x && q && scale && y, MOE_EINVAL, "NULL pointer");
   MOE_REQUIRE(aligned16(x) && aligned16(q), MOE_EINVAL, "x and q must be 16-byte aligned");
-  MOE_REQUIRE(ws_bytes >= fp4_matvec_workspace_bytes(T, N, K), MOE_EWORKSPACE,
-              "workspace smaller than fp4_matvec_workspace_bytes");
   hipStream_t st = as_stream(stream);
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   // rows, tokens of a block
