@@ -572,7 +572,9 @@ moe_status moe_route_backward(const void* grad_out, moe_dtype g_t, const void* d
  *   rstd         device [T] fp32 out: c, for moe_rmsnorm_backward; or NULL
  * A row of zeros with eps == 0 gives NaN, as the formula does.  A row whose
  * sum of squares passes the fp32 range (values of about 2^64 / sqrt(d) and
- * more) gives c = 0 and u = 0; a NaN or an infinity stays in its own row.
+ * more) gives c = 0 and u = 0; with eps == 0 one whose squares all fall below
+ * it (values under 2^-75) gives c = infinity.  A NaN or an infinity stays in
+ * its own row.
  *   Errors: MOE_EINVAL for NULL pointers, bad sizes or types, d % 8 != 0 (d %
  *   128 != 0 with q), a misaligned tensor; MOE_EUNSUPPORTED for d >
  *   MOE_NORM_MAX_D.  T == 0 is valid: nothing is written.

@@ -31,12 +31,13 @@
 // counts itself after its stores have completed.
 //
 // Measured, d = 7168, I = 2048, 256 routed and one shared expert, K = 8: 4-bit
-// weights and one token 64 us, of them logits 5, selection 8, gate/up 24 (5.2
-// TB/s of weights), down 19 (3.7 TB/s); bf16 and 4 tokens 481 to 490 us (5.7
-// TB/s over the call, gate/up and down 6.3 and 6.0); E4M3 and 32 tokens 1264
-// to 1330 us (5.4 to 5.7 TB/s).  The larger ones are bound by the weight
-// stream, whose ceiling with every CU reading is about 6.1 TB/s; one token of
-// 4-bit weights, 218 MB, by four launches' starts and ends, 3 to 4 us each.
+// weights and one token 64 us, of them logits 5, selection 8, gate/up 30 (4.2
+// TB/s of weights), down 22 (3.2 TB/s), 32 tokens 815 us; bf16 and 4 tokens 481
+// to 505 us (5.5 to 5.8 TB/s over the call, gate/up and down 6.0); E4M3 and 32
+// tokens 1264 to 1336 us (5.4 to 5.7 TB/s).  The larger ones are bound by the
+// weight stream, whose ceiling with every CU reading is about 6.1 TB/s; one
+// token of 4-bit weights, 218 MB, by the chain of logits and selection and by
+// the starts and tails of the two products.
 //
 // Measured against one persistent kernel behind the logits (blocks that take
 // gate/up and then down items from queues, a down item waiting for its
@@ -57,7 +58,7 @@ constexpr int FEW_RT = 2;   // 16-row tiles of a product block
 // Steps a product wave's loads run ahead, issued together: an E2M1 step takes
 // half a cache line of a row (4-bit layer, 32 tokens, 812 us against 830 with a
 // step at a time, one token 63.7 against 64.7; E4M3, 32 tokens, 1264 against
-// 1281; bf16 the same).
+// 1281, each pair on one card; bf16 the same).
 constexpr int FEW_D = 2;
 constexpr int LOGIT_W = 8;  // waves of a router block
 constexpr int FEW_THREADS = 64 * FEW_W;
@@ -443,7 +444,10 @@ __device__ __forceinline__ void few_product(const FewArgs& A, int ex, int toks, 
         *reinterpret_cast<sk_f32x4*>(static_cast<float*>(A.h) + o) = sk_f32x4{v[0], v[1], v[2], v[3]};
       } else {
         // h is rounded to bf16, as the operand of the down projection's
-        // matrix instructions (fp32 layers keep it in fp32)
+        // matrix instructions (fp32 layers keep it in fp32).  It is what sets
+        // these layers apart from one with an fp32 h, whose result they are
+        // 1.3e-3 to 2.3e-3 of its norm from (u added, both in bf16); with h
+        // rounded there too, 0 to 2e-4
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.h) + o) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
@@ -611,7 +615,8 @@ bool few_selects_for_itself(const FewArgs& A, int blocks) {
 // Packed where an expert has few tokens: at most two for every routed expert
 // on average, or no more tokens than fit.  (d = 7168, 256 experts, whole
 // layer: E4M3, 32 tokens, 1285 us against 1330; 4-bit, one token, 66 against
-// 69, with the registers held to four waves a SIMD, else 71.)  With more
+// 69, with the registers held to four waves a SIMD, else 71; the form that
+// selects for itself spills 11 of them, 48 bytes of scratch a lane.)  With more
 // tokens an expert the repeated reading of its rows would cost more than the
 // loads of x that it saves.
 template <int WT, typename XT, bool SV>

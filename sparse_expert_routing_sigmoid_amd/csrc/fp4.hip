@@ -90,7 +90,11 @@ __device__ __forceinline__ void mv_store(OT* o, const sk_f32x4& s, int n) {
 
 // One block: RT 16-row tiles of W and up to 16 NT tokens (PK: 4), its waves
 // sharing the K axis.  4096 x 7168 and one token 5.9 us, 2.6 TB/s: launch and
-// one latency of the stream bound it; 16384 x 7168 13 us, 4.8 TB/s.
+// one latency of the stream bound it; 16384 x 7168 16 us, 3.9 TB/s (13 where
+// the 256 MB last-level cache still holds the weights).  More than 4 tokens are
+// bound by x, of which every wave reads its part from L2 for itself, 4 (16
+// tokens) or 8 bytes (32) for a byte of a row tile's weights: 4096 rows 12 and
+// 18 us, 16384 rows 22 and 29.
 constexpr int MV_W = 8;  // waves
 
 template <int RT, int NT, bool SV, bool PK, typename OT>
@@ -150,8 +154,8 @@ __global__ __launch_bounds__(64 * MV_W) void k_fp4_matvec(const uint16_t* __rest
 // consecutive 16-byte words, the lanes' own, so its reads have no bank
 // conflicts.  A step takes half a cache line of each row, so two steps' loads
 // are issued together: apart, the line was fetched twice (65536 x 7168, 16
-// tokens, 62 us; two steps ahead, apart, 58; now 55, of them 48 in the kernel,
-// 5.2 TB/s; 49 with one token).  What a CU takes in at a time bounds it, 20 KB
+// tokens, 62 us; two steps ahead, apart, 58; now 55, 4.6 TB/s; 49 with one
+// token, 5.1 TB/s, 66 with 32).  What a CU takes in at a time bounds it, 18 KB
 // a microsecond: two blocks on one run at half the speed each.
 constexpr int ML_W = 8;   // waves
 
@@ -313,7 +317,9 @@ moe_status fp4_matvec(const void* x, moe_dtype x_t, const uint8_t* q, const uint
     const dim3 grid((unsigned)ceil_div(N, rows), (unsigned)ceil_div(T, tokens));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, xb, q, scale, T, N, K, out);
   };
-  // In us, K = 7168.  Through LDS a CU takes 128 rows at a time in about 27 (up
+  // In us, K = 7168 (the limits hold for every K; at others they were not
+  // measured; up to 16384 rows the weights came from the last-level cache, from
+  // memory these calls take up to a quarter longer).  Through LDS a CU takes 128 rows at a time in about 27 (up
   // to 16 tokens; 32 tokens 34) and 256 in twice that, however many of its
   // neighbours have none left: `units` of 32768 rows, with one row tile to a wave
   // when their number is odd (81920 rows, 16 tokens, 86, with two tiles 105), else

@@ -6,13 +6,19 @@
 //                          dw_j = sum_t du_tj xhat_tj
 // Both are bound by HBM: every operand is read once and every result written
 // once, the row living in registers between the reduction and its use (a
-// thread holds C chunks of 8 columns; TPR threads share a row).  A thread
-// has read all it needs of a row before it writes any of it, so a result may
-// lie on an operand of its own type.
+// thread holds C chunks of 8 columns; TPR threads share a row).  Up to d = 8192
+// nothing spills; of the forms beyond, most that have an fp32 operand do: the
+// forward's for d > 16384 6 to 46 registers, the backward's 4 to 18, which
+// live in scratch memory for that time.  A thread has read all it needs of a
+// row before it writes any of it, so a result may lie on an operand of its own
+// type.
 // Measured, bf16: forward, 16384 rows of 7168, 173 us without tiles (5.4 TB/s
-// of a half read, half written mix; a large copy reaches 4.8), 187 with them
-// (5.7 TB/s), one row 2.8 us; backward 144 us (6.5 TB/s of three reads and a
-// write), 8192 rows 93 us with k_norm_dw.
+// of a half read, half written mix; a large copy reaches 4.8), 183 to 187 with
+// them (5.7 TB/s), one row 2.8 us; backward 144 us (6.5 TB/s of three reads and
+// a write), 8192 rows 93 us with k_norm_dw.  Few rows of wide d are the
+// farthest from the bytes they need, since every block leaves a row of dw sums:
+// 7168 columns, 256 rows 12.5 us for 3.1 of copying, 1024 rows 22 for 12, 2048
+// rows 33 for 25.
 #include "common.h"
 #include "vec8.h"
 
