@@ -817,6 +817,7 @@ class LatentCache:
         self.n_failed = torch.zeros((1,), **i32)
         self.cu_new = torch.zeros((B + 1,), **i32)
         self.slot, self.position = (torch.full((max_tokens,), -1, **i32) for _ in range(2))
+        self.rows = 0                                              # of the last extend(): slots behind are older ones
         self.pages_ws = torch.empty((max(mla_pages_workspace_bytes(B), 1),), dtype=torch.uint8, device=dev)
         need = [mla_decode_workspace_bytes(B, i, H, dn, dr, dv, dc, self.max_len) for i in range(1, S + 1)]
         self.ws = torch.empty((max(need + [1]),), dtype=torch.uint8, device=dev)
@@ -832,13 +833,15 @@ class LatentCache:
         slot, position = self.slot[:tokens], self.position[:tokens]
         mla_pages_extend(self.seq_len, new_len, self.page_size, self.block_table, self.free_pages, self.n_free,
                          self.seq_len, self.n_free, self.n_failed, self.cu_new, slot, position, self.pages_ws, stream)
+        self.rows = tokens
         return slot, position
 
     def write(self, latent, k_rope, layer=0, stream=None):
-        """Rows of the last extend() into a layer's cache: latent [n, dc], k_rope [n, dr]."""
+        """Rows of the last extend() (the replay of a captured call is none)
+        into a layer's cache: latent [n, dc], k_rope [n, dr], n at most its `tokens`."""
         n = latent.shape[0]
-        if n > self.max_tokens:
-            raise ValueError(f"latent: at most {self.max_tokens} rows")
+        if n > self.rows:
+            raise ValueError(f"latent: {n} rows, of which the last extend() placed {self.rows}")
         mla_cache_write(latent, k_rope, self.slot[:n], self.cache[layer], stream)
 
     def decode(self, q, w_kv, scale, out, S=1, layer=0, stream=None):
