@@ -717,7 +717,8 @@ moe_status moe_layer_few(const void* u, moe_dtype u_t, const float* centroids, c
  * the i-th page that the step takes is free_pages[n_free - 1 - i].  A request
  * whose tokens need more than table_width pages, more free pages than those
  * before it left (it is counted with them all the same), or rows past N is not
- * served: it gets no page, its length stays and its tokens get slot -1.
+ * served: it gets no page, its length stays and its tokens get slot -1.  A
+ * request without new tokens needs none of these and is always served.
  *   seq_len, new_len  device [B] int32 (values below 0 count as 0)
  *   block_table       device [B, table_width] int32, in and out: the first
  *                     ceil(seq_len / page_size) entries of a row are read, the

@@ -88,7 +88,7 @@ def pages_extend(seq_len, new_len, page, table, free, n_free, N):
         old, add = max(0, old), max(0, add)
         have, want = -(-old // page), -(-(old + add) // page)
         need = want - have
-        room = want <= W and cu[-1] + add <= N
+        room = add == 0 or (want <= W and cu[-1] + add <= N)
         ok = room and (need == 0 or taken + need <= n_free)
         if ok:
             for i in range(need):

@@ -113,6 +113,7 @@ __global__ __launch_bounds__(PG_THREADS) void k_pages_extend(PageArgs a, PagePla
   };
   auto need = [&](int old, int add, long long cu) -> int {  // pages, or -1 for a request that can't be served
     const long long len = (long long)old + add;
+    if (add == 0) return 0;
     if (len > 0x7FFFFFFF || cu + add > a.N) return -1;
     const int have = (int)(((uint32_t)old + a.P - 1u) / a.P), want = (int)(((uint32_t)len + a.P - 1u) / a.P);
     return want <= a.W ? want - have : -1;
