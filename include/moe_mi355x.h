@@ -791,8 +791,8 @@ moe_status mla_cache_write(const void* latent, long long ld_latent, const void* 
  *   out, out_t   device [B, S, H, dv] out, MOE_F32 or MOE_BF16
  *   ws           device, mla_decode_workspace_bytes(...) bytes
  * A page outside [0, n_pages) among those of a request's tokens, or a length
- * past table_width * page_size, makes the request's outputs NaN; no memory
- * outside the cache is read.  A NaN or an infinity in a cached row reaches the
+ * past table_width * page_size or 2^31 - 256, makes the request's outputs NaN; no
+ * memory outside the cache is read.  A NaN or an infinity in a cached row reaches the
  * tokens that see it and, with S > 1, may reach those of the same request that
  * do not; it stays in its request.  Memory behind a request's last token does
  * not matter.

@@ -43,6 +43,9 @@ typedef const __attribute__((address_space(4))) int32_t const_i32;  // read by s
 
 constexpr int DEC_MAX_B = 8192, DEC_TILE = 64, DEC_CUS = 256;
 constexpr long long DEC_MAX_ROWS = 1LL << 26;  // B S H: k_absorb's grid stays below 2^32 threads
+// Tiles are rounded up and loads run two halves ahead, 190 tokens past a request's
+// last at most: numbers of tokens then stay in 31 bits.
+constexpr long long DEC_MAX_LEN = (1LL << 31) - 256;
 
 struct DecArgs {
   const uint16_t *q, *w, *cache;
@@ -60,7 +63,7 @@ struct DecArgs {
 };
 
 __device__ __forceinline__ int dec_len(const DecArgs& a, int seq) {
-  return min(max(seq, 0), (int)min((long long)a.W * a.P, 0x7FFFFFFFLL));
+  return min(max(seq, 0), (int)min((long long)a.W * a.P, DEC_MAX_LEN));
 }
 
 // Of G workers (as many as there are tiles, at most), w takes tiles
