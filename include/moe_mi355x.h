@@ -705,7 +705,7 @@ moe_status moe_layer_few(const void* u, moe_dtype u_t, const float* centroids, c
  * with dn values in the first part of a key and dv in a value.  A cache keeps
  * c and r only.  dn, dr, dv and dc are multiples of 8, dn and dv <= 128,
  * dr <= 64, dc <= 512; the rotations are the caller's.  scale is positive and
- * finite.
+ * at most 2^127.
  * ====================================================================== */
 
 /* ------------------------------------------------------------------------

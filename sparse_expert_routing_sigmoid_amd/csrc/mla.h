@@ -34,6 +34,7 @@ inline bool mla_dims_ok(int dn, int dr, int dv) {
   return dn >= 8 && dn % 8 == 0 && dn <= MLA_MAX_DN && dr >= 8 && dr % 8 == 0 && dr <= MLA_MAX_DR && dv >= 8 &&
          dv % 8 == 0 && dv <= MLA_MAX_DV;
 }
+inline bool mla_scale_ok(float scale) { return scale > 0.f && scale <= 0x1p127f; }  // scale * LOG2E is finite
 inline bool mla_dc_ok(int dc) { return dc >= 8 && dc % 8 == 0 && dc <= MLA_MAX_DC; }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mla_rsrc(const void* base, uint32_t bytes) {

@@ -42,7 +42,7 @@ inline moe_status attn_check(const char* where, const void* q, const void* kv, c
   const long long tiles = (Tq > Tk ? Tq : Tk) / 128 + B;
   if (tiles * H > ATTN_MAX_TILES || Tk * dr > (1LL << 33))
     return bad(MOE_EUNSUPPORTED, "more than 2^22 tiles of 128 rows and a head, or 2^33 values in k_rope");
-  if (!(std::isfinite(scale) && scale > 0.f)) return bad(MOE_EINVAL, "scale must be positive and finite");
+  if (!mla_scale_ok(scale)) return bad(MOE_EINVAL, "scale must be positive and at most 2^127");
   if (!(ldr >= dr && ldr % 8 == 0 && ldr <= (1 << 20)))
     return bad(MOE_EINVAL, "k_rope's row stride must be a multiple of 8 that holds a row, at most 2^20");
   if (Tq > 0 && B > 0 && !(q && cu_q && cu_k && (Tk == 0 || (kv && k_rope)))) return bad(MOE_EINVAL, "NULL pointer");

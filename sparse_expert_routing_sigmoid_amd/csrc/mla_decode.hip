@@ -636,7 +636,7 @@ moe_status decode(const void* q, const void* w, const void* cache, long long n_p
               "more requests than MLA_MAX_REQUESTS, S above 64 or H above 1024");
   MOE_REQUIRE(n_pages * page_size < (1LL << 31), MOE_EUNSUPPORTED, "2^31 slots or more");
   MOE_REQUIRE((long long)B * S * H <= DEC_MAX_ROWS, MOE_EUNSUPPORTED, "more than 2^26 queries");
-  MOE_REQUIRE(std::isfinite(scale) && scale > 0.f, MOE_EINVAL, "scale must be positive and finite");
+  MOE_REQUIRE(mla_scale_ok(scale), MOE_EINVAL, "scale must be positive and at most 2^127");
   MOE_REQUIRE(out_t == MOE_F32 || out_t == MOE_BF16, MOE_EINVAL, "out_t must be MOE_F32 or MOE_BF16");
   if (B == 0) return MOE_OK;
   MOE_REQUIRE(q && w && table && seq_len && out && cache && n_pages > 0, MOE_EINVAL, "NULL pointer");
