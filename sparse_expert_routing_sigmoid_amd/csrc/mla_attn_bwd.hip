@@ -9,8 +9,9 @@
 // powers of two), k_attn_dkv walks the queries of 128 keys.  That is seven
 // products of 2 dqk or 2 dv flops a visible pair and head, 2 (4 dqk + 3 dv), where
 // five, 2 (3 dqk + 2 dv), would do if dQ were added up across blocks: by atomics,
-// whose order changes the sums' bits, or from parts in memory, more bytes than the
-// two products take time.  P and dS are rounded to bf16 for their products, to
+// whose order changes the sums' bits, or from dS kept in memory, 2 GB of bf16 at
+// 4096 tokens and 128 heads.  (A head's causal half of that is 16 MB, so a few heads
+// at a time would stay in the last-level cache: not measured.)  P and dS are rounded to bf16 for their products, to
 // the nearest (2^-8 of a term at most, of either sign; the sums stay fp32).
 // k_attn_dr adds the heads' parts of dr, which k_attn_dkv leaves in fp32.
 #include <type_traits>
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnArgs a, const uint16_t* 
 // issues while the other waits.  Query tiles are staged four deep: the second
 // wave is one behind, and two are in flight.
 // 4096 tokens, 128 heads, causal: 1555 us, 885 TFLOP/s of these products; the MFMA
-// pipe is busy 45 % of the cycles at 1.9 GHz.  Measured against it: one wave of 32
+// pipe is busy 46 % of the cycles at 1.9 GHz.  Measured against it: one wave of 32
 // keys and all four products a SIMD, with every fragment read ahead and the
 // arithmetic spread between the products, 1581 us; pairs on 64 keys, one wave a
 // SIMD, 1667; dK added up a step later, so that one kind's products run beside
@@ -396,7 +397,9 @@ moe_status attention_backward(const void* dout, const void* q, const void* kv, c
       hipLaunchKernelGGL(kkv, dim3((unsigned)(8 * a.per_xcd)), dim3(512), 0, s, a, g, stat, dkv, bf16, part);
     }
   };
-  if (dn <= 64 && dr <= 32 && dv <= 64)  // as in the forward
+  // as in the forward: 2 sequences of about 2000, 32 heads of 64 + 32, 456 us for 642;
+  // 8 of about 1000, 64 heads of 40 + 24, 623 for 827
+  if (dn <= 64 && dr <= 32 && dv <= 64)
     go(k_attn_dq<64, 32, 64>, k_attn_dkv<64, 32, 64>);
   else
     go(k_attn_dq<128, 64, 128>, k_attn_dkv<128, 64, 128>);

@@ -24,13 +24,18 @@
 // S^T = C Q~^T and O~^T = C^T P^T both read the staged rows of the cache
 // (mla.h), which are read from memory once for 32 RG rows.
 //
-// Up to 64 rows the cache's bytes bound k_decode: 3.2 us for a visit of a tile on
-// every CU at once, 5.9 TB/s, of which the products alone take 1.9.  With more rows
-// a tile is visited by a block for each 64, the second time out of the L2, and a
-// visit takes 2.2 to 2.8 us.  Measured (k_absorb + k_decode + k_out, us): one
-// request of 200 tokens, 8 heads: 3 + 11 + 8.5; one of 131072, 128 heads: 5 + 59 +
-// 14; 31 of about 6000, 8 heads, 4 tokens each: 5 + 55 + 11; 128 of about 8000, 128
-// heads: 13 + 356 + 27.
+// With work for every CU k_decode's time is a start, a visit of a tile by every CU
+// at once so many times, and the requests that a run crosses into.  32 rows: 17 us
+// to start (the first loads and q~ behind the search for the request, two more
+// barriers in the first tile, the piece's stores), 2.45 a visit where the rows come
+// from the last-level cache and 3.3 where they come from memory (302 MB at 5.8
+// TB/s), 8.5 for a crossing (loads, q~ and stores once more, nothing under them).  64
+// rows: 21, 2.05 (2.2 to 2.8 in a large batch, whose tiles a block for each 64 rows
+// visits, the second out of the L2) and 9; the products alone take 1.9 of a visit.
+// Measured (k_absorb + k_decode + k_out, us): one request of 200 tokens, 8 heads: 3
+// + 11 + 8.5; one of 131072, 128 heads: 5 + 57 + 14; 31 of about 6000, 8 heads, 4
+// tokens each: 5 + 54 + 11 (a start, ten more visits and a crossing); 128 of about
+// 8000, 128 heads: 13 + 358 + 27.
 #include <type_traits>
 
 #include "mla.h"
@@ -71,7 +76,10 @@ __device__ __forceinline__ int dec_len(const DecArgs& a, int seq) {
 __device__ __forceinline__ int dec_workers(const DecArgs& a, long long T) { return (int)min((long long)a.workers, T); }
 __device__ __forceinline__ int dec_worker(long long t, long long T, int G) { return (int)(((t + 1) * G - 1) / T); }
 
-// q~ for 32 tokens, a head and 128 columns; block 0 also numbers the tiles.
+// q~ for 32 tokens, a head and 128 columns; block 0 also numbers the tiles.  128
+// tokens of 128 heads: 13 us, of which 51 MB from and to memory take 10.5 at a
+// copy's rate.  8-byte accesses to q and q~, whose rows 16 apart share their banks,
+// conflict (39 % of the LDS cycles).
 __global__ __launch_bounds__(256) void k_absorb(DecArgs a) {
   __shared__ __align__(16) uint8_t lds[128 * 256 + 32 * 256];
   __shared__ long long sum[4];
@@ -198,7 +206,10 @@ __device__ __forceinline__ int dec_request(const long long* first, int B, long l
 // request's last row (later rows read as zeros).  Chunks past dc in a row's last
 // 16 are r's and the next row's, which meet zeros of q~ and columns that are not
 // kept.  ANY: other page sizes; each row is then looked up by itself (pages of
-// 100 against 64, 16384 tokens, 128 heads: 104 against 82 us).
+// 100 against 64, 131072 tokens, 128 heads: k_decode 81 against 57 us, with latents
+// of 136 61 against 36).  A row takes 1024 bytes of LDS whatever dc is, so latents of
+// 256 and fewer have the same visits at half the bytes and products (131072 tokens,
+// 128 heads: 38 us of 256, 36 of 136).
 template <int RG, int DC, bool ANY>
 __global__ __launch_bounds__(256, 1) void k_decode(DecArgs a) {
   constexpr int XN = 4 / RG, CS = DC / 16, RS = 4, OT = DC / 32 / XN, ROWS = DEC_HALF / 4;
@@ -658,7 +669,7 @@ moe_status decode(const void* q, const void* w, const void* cache, long long n_p
     hipLaunchKernelGGL(kernel, dim3((unsigned)(ceil_div(p.workers, 8) * 8 * p.row_blocks)), dim3(256), 0, st, a);
   };
   // latents up to 256 by kernels of half the registers and products: 16384 tokens of
-  // 256, 128 heads, 30.6 us a call for 36.2
+  // 256, 128 heads, 31 us a call for 36, 131072 52 for 63
   auto pick = [&](auto any) {
     constexpr bool ANY = decltype(any)::value;
     if (dc <= 256) {

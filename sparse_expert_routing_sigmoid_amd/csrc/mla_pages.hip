@@ -172,7 +172,8 @@ __global__ __launch_bounds__(256) void k_pages_tokens(PageArgs a, const PagePlan
 }
 
 // One block: pages of the requests marked in `done` onto the stack, in the
-// order of requests and pages; their lengths to zero.
+// order of requests and pages; their lengths to zero.  64 requests of 64 pages: 4.6
+// us; 509 of 32: 15.4, a request to a wave 32 times in turn.
 __global__ __launch_bounds__(PG_THREADS) void k_pages_release(const int32_t* __restrict__ done, int32_t* seq_len, int B,
                                                               int P, const int32_t* __restrict__ table, int W,
                                                               int32_t* free_pages, int F, int32_t* n_free) {
